@@ -57,10 +57,14 @@ typedef enum {
   TILEMIX_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed       */
   TILEMIX_ERR_TIMEOUT = 4,      /* device: a pipeline wait ran too long    */
   TILEMIX_ERR_BAD_SEQLENS = 5,  /* device: cu_seqlens or head_map invalid  */
-  TILEMIX_ERR_NO_DEVICE = 6     /* current device is not sm_100            */
+  TILEMIX_ERR_NO_DEVICE = 6,    /* current device is not sm_100            */
+  TILEMIX_ERR_BAD_PAGES = 7     /* device: a page table entry out of range */
 } tilemix_status;
 
 enum { TILEMIX_KV_FP16 = 0, TILEMIX_KV_INT8 = 1 };
+
+/* 16-bit element types of the paged-cache calls. */
+enum { TILEMIX_FP16 = 0, TILEMIX_BF16 = 1 };
 
 /* Ignore the routing words: every legal tile takes the FP16 path and the
  * INT8 operands (q8, q_scale, and k8, k_scale for TILEMIX_KV_FP16) may be
@@ -396,6 +400,238 @@ typedef struct {
  */
 tilemix_status tilemix_attn_prefill(const tilemix_attn_params* params,
                                     tilemix_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Rotary positions and the paged KV cache
+ *
+ * What a serving loop does around the prefill attention: rotate Q and K,
+ * write K and V of the new tokens into the pages of a cache, and attend the
+ * new tokens (a prompt's next chunk, one decoded token, a few drafted ones)
+ * over everything the cache holds.
+ *
+ * The cache.  A page holds `page_size` consecutive positions of one sequence
+ * for every KV head.  k_pages and v_pages are strided arrays of
+ * [num_pages][page_size][hkv][head_dim] elements, channels contiguous:
+ * element (page, slot, head, c) lies at
+ *   page * page_stride + slot * token_stride + head * head_stride + c
+ * (elements; the same strides for K and V), so pages may be laid out token-
+ * or head-major, or interleave K and V.  Position p of sequence b lies in
+ * page page_table[b * table_stride + p / page_size], slot p % page_size.
+ * The rest of a table row is never read.  Pages hold the 16-bit type of the
+ * call, or INT8 codes (TILEMIX_KV_INT8) with one fp32 scale per (token,
+ * head) in k_scale / v_scale [num_pages][hkv][page_size]: a token's codes
+ * never change when later tokens join its page, unlike block scales.
+ *
+ * New tokens.  cu_seqlens (dev int32 [batch + 1], as for the prefill calls)
+ * delimits each sequence's new tokens in the token-major tensors; rows at or
+ * past cu_seqlens[batch] are padding, neither read nor written.  kv_lens
+ * (dev int32 [batch]) is each sequence's cache length AFTER its new tokens
+ * joined; the same array serves the append and the attention.
+ *
+ * Device-side checks (status word): BAD_SEQLENS for a cu_seqlens that
+ * decreases or leaves [0, total_tokens], or a kv_lens entry that is negative
+ * or above what the table row can hold (or max_kv_len); BAD_PAGES for a page
+ * table entry in use outside [0, num_pages).  The sequences (for the append:
+ * the tokens) that show the problem keep their outputs as they were.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Frequency scalings of tilemix_rope_frequencies. */
+enum {
+  TILEMIX_ROPE_SCALE_NONE = 0,
+  TILEMIX_ROPE_SCALE_LINEAR = 1,      /* positions divided by factor        */
+  TILEMIX_ROPE_SCALE_NTK = 2,         /* base raised                        */
+  TILEMIX_ROPE_SCALE_WAVELENGTH = 3,  /* long wavelengths divided by factor */
+  TILEMIX_ROPE_SCALE_YARN = 4         /* by rotations, with attn_factor     */
+};
+
+/*
+ * Host helper: the rotary frequencies (radians per position) of a model's
+ * configuration, in double.  No counterpart in the TileMix pages.
+ * With f_i = base^(-2i / rot_dim), i = 0 .. rot_dim/2 - 1, and N =
+ * original_max_position:
+ *   NONE        f_i
+ *   LINEAR      f_i / factor
+ *   NTK         f_i with base * factor^(rot_dim / (rot_dim - 2)); rot_dim > 2
+ *   WAVELENGTH  with low = low_freq_factor, high = high_freq_factor, w =
+ *               2 pi / f_i: t = clamp((N / w - low) / (high - low), 0, 1),
+ *               (1 - t) f_i / factor + t f_i
+ *   YARN        with c(n) = rot_dim ln(N / (2 pi n)) / (2 ln base), lo =
+ *               max(floor(c(high_freq_factor)), 0), hi =
+ *               min(ceil(c(low_freq_factor)), rot_dim - 1) (high_freq_factor
+ *               and low_freq_factor: rotations over N, e.g. 32 and 1), t =
+ *               clamp((i - lo) / max(hi - lo, 0.001), 0, 1): t f_i / factor
+ *               + (1 - t) f_i, attn_factor = 0.1 ln(factor) + 1 for factor > 1
+ * attn_factor is 1 for the others.  `freqs` is a HOST array of rot_dim / 2
+ * doubles; the caller copies it to the device.  Touches no device.
+ * Errors: INVALID_ARG for a null freqs, rot_dim not positive and even,
+ * base <= 1, factor <= 0, or (WAVELENGTH, YARN) N <= 0 or
+ * 0 < low_freq_factor < high_freq_factor not satisfied.
+ */
+tilemix_status tilemix_rope_frequencies(int scaling, int rot_dim, double base,
+                                        double factor, double low_freq_factor,
+                                        double high_freq_factor,
+                                        int original_max_position,
+                                        double* freqs, float* attn_factor);
+
+/* Which channels form pair i of the rotated part. */
+enum {
+  TILEMIX_ROPE_HALF = 0,        /* channels i and i + rot_dim / 2 */
+  TILEMIX_ROPE_INTERLEAVED = 1  /* channels 2i and 2i + 1         */
+};
+
+/* Arguments of tilemix_rope.  Zero-initialise, set struct_size. */
+typedef struct {
+  uint32_t struct_size;
+  int dtype;                 /* TILEMIX_FP16 or TILEMIX_BF16                */
+  int layout;                /* TILEMIX_ROPE_*                              */
+  int inverse;               /* 1: rotate by the negative angle             */
+  /* [T, hq, d] and [T, hkv, d], channels contiguous, token and head strides
+   * in elements (multiples of 8), 16-byte aligned bases.  k may be NULL (hkv
+   * is then ignored).  An output equal to its input (same strides) rotates
+   * in place; any other overlap is undefined. */
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+  int64_t q_out_stride_t, q_out_stride_h, k_out_stride_t, k_out_stride_h;
+  const int32_t* positions;  /* dev int32 [T]                               */
+  const double* freqs;       /* dev double [rot_dim / 2], radians/position  */
+  float attn_factor;         /* multiplies cos and sin; 0 = 1               */
+  int total_tokens, hq, hkv;
+  int head_dim;              /* multiple of 16, <= 256                      */
+  int rot_dim;               /* multiple of 16, in [16, head_dim]           */
+} tilemix_rope_params;
+
+/*
+ * Rotary positions of Q and K in one launch.  No counterpart in the TileMix
+ * pages, which start from rotated Q and K.
+ * For token t, every head and pair i with channels (a, b):
+ *   c = attn_factor cos(positions[t] freqs[i]), s = attn_factor sin(...)
+ *   y_a = x_a c - x_b s,  y_b = x_b c + x_a s
+ * (inverse: s negated, which with attn_factor = 1 undoes the rotation and in
+ * every case is its gradient: dL/dx is the inverse rotation of dL/dy).
+ * Channels rot_dim .. head_dim - 1 are copied.  Angles are formed and reduced
+ * in double, so far positions stay exact; products are fp32, rounded once.
+ */
+tilemix_status tilemix_rope(const tilemix_rope_params* params,
+                            tilemix_stream_t stream);
+
+/* Arguments of tilemix_paged_append.  Zero-initialise, set struct_size. */
+typedef struct {
+  uint32_t struct_size;
+  int dtype;                 /* of k, v, q: TILEMIX_FP16 or TILEMIX_BF16    */
+  int kv_format;             /* TILEMIX_KV_FP16: pages hold dtype; _INT8    */
+  int layout;                /* TILEMIX_ROPE_* (with freqs)                 */
+  /* New tokens: [T, hkv, d]; q optional [T, hq, d] with q_out (rotated like
+   * k; needs freqs).  Strides as for tilemix_rope. */
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  int64_t q_stride_t, q_stride_h, q_out_stride_t, q_out_stride_h;
+  const int32_t* positions;  /* optional dev int32 [T]: rotary positions;
+                                NULL: each token's position in the cache    */
+  const double* freqs;       /* optional dev double [rot_dim / 2]; NULL: K is
+                                written as it is                            */
+  void* k_pages;
+  void* v_pages;
+  int64_t page_stride, token_stride, head_stride;  /* elements, multiples of
+                                8 (16-bit) or 16 (INT8)                     */
+  float* k_scale;            /* TILEMIX_KV_INT8: [num_pages][hkv][page_size] */
+  float* v_scale;
+  const int32_t* page_table; /* dev int32 [batch][table_stride]             */
+  int64_t table_stride;      /* >= max_pages                                */
+  const int32_t* cu_seqlens;
+  const int32_t* kv_lens;
+  int batch, total_tokens, hq, hkv;
+  int head_dim;              /* 64 or 128                                   */
+  int rot_dim;               /* with freqs: multiple of 16 in [16, head_dim] */
+  int num_pages, page_size, max_pages;  /* page_size a power of two in
+                                [16, 256]; max_pages: entries of a table row */
+  float attn_factor;         /* 0 = 1                                       */
+  int32_t* status;           /* optional                                    */
+} tilemix_append_params;
+
+/*
+ * Write the new tokens' K and V into the pages, rotating K (and Q) on the
+ * way, in one launch.  No counterpart in the TileMix pages (appendix C keeps
+ * its INT8 KV cache as one prefilled tensor).
+ * New token i of sequence b (n_b of them) goes to position kv_lens[b] - n_b
+ * + i.  With freqs, K and Q are rotated exactly as tilemix_rope does and
+ * rounded to dtype; INT8 pages then hold, per (token, head), a = max |x| over
+ * the d channels of that 16-bit row, scale = a / 127 (IEEE fp32 division),
+ * code = clamp(round_half_even(x / scale), -127, 127), scale 0 and codes 0
+ * for a = 0 (the definition of tilemix_quantize_blockwise with blocks of one
+ * token).  Two tokens of one call that map to the same page slot race.
+ */
+tilemix_status tilemix_paged_append(const tilemix_append_params* params,
+                                    tilemix_stream_t stream);
+
+/* Arguments of tilemix_attn_paged.  Zero-initialise, set struct_size. */
+typedef struct {
+  uint32_t struct_size;
+  int dtype;                 /* of q and out: TILEMIX_FP16 or TILEMIX_BF16  */
+  int kv_format;             /* TILEMIX_KV_FP16: pages hold dtype; _INT8    */
+  int causal;                /* 1: query i sees positions <= its own;
+                                0: every position below kv_lens[b]          */
+  const void* q;             /* [T, hq, d], strides as for tilemix_rope     */
+  int64_t q_stride_t, q_stride_h;
+  const void* k_pages;
+  const void* v_pages;
+  int64_t page_stride, token_stride, head_stride;
+  const float* k_scale;      /* TILEMIX_KV_INT8                             */
+  const float* v_scale;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* cu_seqlens;
+  const int32_t* kv_lens;
+  int batch, total_tokens;
+  int max_q_len;             /* host: >= every sequence's new tokens        */
+  int max_kv_len;            /* host: >= every kv_lens entry                */
+  int hq, hkv;               /* hq % hkv == 0, hq / hkv <= 128; query head h
+                                reads KV head h / (hq / hkv)                */
+  int head_dim;              /* 64 or 128                                   */
+  int num_pages, page_size, max_pages;
+  float softmax_scale;       /* <= 0 means 1 / sqrt(head_dim)               */
+  void* out;                 /* [T, hq, d] contiguous                       */
+  float* lse;                /* optional fp32 [hq, T]: natural-log LSE      */
+  void* workspace;           /* dev scratch, 16-byte aligned; see below     */
+  size_t workspace_bytes;
+  int32_t* status;           /* optional                                    */
+} tilemix_attn_paged_params;
+
+/*
+ * Bytes of scratch tilemix_attn_paged needs for these shapes (it holds the
+ * partial results of sequences whose keys several blocks share).  It does
+ * not depend on batch or lengths beyond max_q_len, needs no initialisation,
+ * and must not be shared by two calls that may run at the same time (two
+ * streams, two graphs replayed together).  Host only; 0 for sizes
+ * tilemix_attn_paged refuses.  No counterpart in the TileMix pages.
+ */
+size_t tilemix_attn_paged_workspace_bytes(int max_q_len, int hq, int hkv,
+                                          int head_dim);
+
+/*
+ * Attention of the new tokens over the paged cache (forward).  No counterpart
+ * in the TileMix pages; the softmax state is that of tilemix_attn_prefill
+ * (section 3 Preliminaries).
+ * For new token i of sequence b (n_b of them, L = kv_lens[b]), query head h
+ * and its KV head:
+ *   keys j < L, and with causal = 1 only j <= L - n_b + i
+ *   s_ij = softmax_scale q_i . k_j,  out_i = sum_j softmax_j(s_i.) v_j,
+ *   lse_i = ln sum_j exp(s_ij);  a row without a key: out 0, lse -inf
+ * where INT8 pages stand for k = code * k_scale, v = code * v_scale, exactly.
+ * Products run on tensor cores with fp32 accumulation; P is rounded to dtype
+ * (INT8 pages: to fp16).  Slots of a page past a sequence's length may hold
+ * anything, NaN included.  Results do not depend on page placement; the
+ * order of summation depends on the batch's lengths, not on timing.
+ */
+tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* params,
+                                  tilemix_stream_t stream);
 
 /* Static description of a status code. */
 const char* tilemix_status_string(tilemix_status status);

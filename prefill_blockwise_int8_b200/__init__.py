@@ -17,6 +17,12 @@ Entry points (same names as the C ABI):
   tilemix_pack_mask(route, cu_seqlens, max_seqlen, block_m, block_n, group)
       -> mask
   tilemix_attn_prefill(q, k, v, cu_seqlens, max_seqlen, ...) -> out
+  tilemix_rope_frequencies(rot_dim, base, ...) -> (freqs, attn_factor)
+  tilemix_rope(q, k, positions, freqs, ...) -> (q_out, k_out)
+  tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
+      v_pages, ...) -> rotated q or None
+  tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
+      max_q_len, max_kv_len, ...) -> out
 """
 from __future__ import annotations
 
@@ -32,7 +38,9 @@ __all__ = [
     "ROUTE_ADAPTIVE_STATIC_BYTES", "tilemix_status_string",
     "tilemix_last_error", "tilemix_version", "KV_FP16", "KV_INT8", "FLAG_FP16_ONLY",
     "FLAG_QUANT_ON_CHIP", "FLAG_TEST_EXPIRE_WAIT", "FLAG_PV_F16_ACC", "STATUS",
-    "LAYOUTS",
+    "LAYOUTS", "tilemix_rope_frequencies", "tilemix_rope",
+    "tilemix_paged_append", "tilemix_attn_paged",
+    "tilemix_attn_paged_workspace_bytes", "ROPE_LAYOUTS", "ROPE_SCALINGS",
 ]
 
 _LIB_PATH = Path(__file__).resolve().parent / "libtilemix.so"
@@ -45,11 +53,16 @@ FLAG_PV_F16_ACC = 8  # study only: O accumulated in fp16 (no tolerance)
 STATUS = {0: "TILEMIX_OK", 1: "TILEMIX_ERR_INVALID_ARG",
           2: "TILEMIX_ERR_UNSUPPORTED", 3: "TILEMIX_ERR_CUDA",
           4: "TILEMIX_ERR_TIMEOUT", 5: "TILEMIX_ERR_BAD_SEQLENS",
-          6: "TILEMIX_ERR_NO_DEVICE"}
+          6: "TILEMIX_ERR_NO_DEVICE", 7: "TILEMIX_ERR_BAD_PAGES"}
 
 # Routing-template layouts (TILEMIX_LAYOUT_*).
 LAYOUTS = {"all_fp16": 0, "all_int8": 1, "band": 2, "global": 3,
            "row_random": 4, "aligned": 5, "bigbird": 6, "sptrans": 7}
+
+# Rotary pair layouts (TILEMIX_ROPE_*) and frequency scalings
+# (TILEMIX_ROPE_SCALE_*).
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "wavelength": 3, "yarn": 4}
 
 # Every function include/tilemix.h declares.
 EXPORTED_SYMBOLS = (
@@ -57,6 +70,8 @@ EXPORTED_SYMBOLS = (
     "tilemix_pack_mask", "tilemix_attn_prefill",
     "tilemix_route_template", "tilemix_route_adaptive_workspace_bytes",
     "tilemix_route_adaptive", "tilemix_route_adaptive_noalloc",
+    "tilemix_rope_frequencies", "tilemix_rope", "tilemix_paged_append",
+    "tilemix_attn_paged_workspace_bytes", "tilemix_attn_paged",
     "tilemix_status_string", "tilemix_last_error", "tilemix_version",
 )
 
@@ -89,6 +104,73 @@ class AttnParams(C.Structure):
         ("softmax_scale", C.c_float), ("causal", C.c_int),
         ("out", C.c_void_p), ("lse", C.c_void_p), ("qk_dump", C.c_void_p),
         ("status", C.c_void_p),
+    ]
+
+
+class RopeParams(C.Structure):
+    """Mirror of tilemix_rope_params (include/tilemix.h)."""
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("dtype", C.c_int), ("layout", C.c_int),
+        ("inverse", C.c_int),
+        ("q", C.c_void_p), ("k", C.c_void_p), ("q_out", C.c_void_p),
+        ("k_out", C.c_void_p),
+        ("q_stride_t", C.c_int64), ("q_stride_h", C.c_int64),
+        ("k_stride_t", C.c_int64), ("k_stride_h", C.c_int64),
+        ("q_out_stride_t", C.c_int64), ("q_out_stride_h", C.c_int64),
+        ("k_out_stride_t", C.c_int64), ("k_out_stride_h", C.c_int64),
+        ("positions", C.c_void_p), ("freqs", C.c_void_p),
+        ("attn_factor", C.c_float), ("total_tokens", C.c_int),
+        ("hq", C.c_int), ("hkv", C.c_int), ("head_dim", C.c_int),
+        ("rot_dim", C.c_int),
+    ]
+
+
+class AppendParams(C.Structure):
+    """Mirror of tilemix_append_params (include/tilemix.h)."""
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("dtype", C.c_int),
+        ("kv_format", C.c_int), ("layout", C.c_int),
+        ("k", C.c_void_p), ("v", C.c_void_p), ("q", C.c_void_p),
+        ("q_out", C.c_void_p),
+        ("k_stride_t", C.c_int64), ("k_stride_h", C.c_int64),
+        ("v_stride_t", C.c_int64), ("v_stride_h", C.c_int64),
+        ("q_stride_t", C.c_int64), ("q_stride_h", C.c_int64),
+        ("q_out_stride_t", C.c_int64), ("q_out_stride_h", C.c_int64),
+        ("positions", C.c_void_p), ("freqs", C.c_void_p),
+        ("k_pages", C.c_void_p), ("v_pages", C.c_void_p),
+        ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+        ("head_stride", C.c_int64),
+        ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+        ("page_table", C.c_void_p), ("table_stride", C.c_int64),
+        ("cu_seqlens", C.c_void_p), ("kv_lens", C.c_void_p),
+        ("batch", C.c_int), ("total_tokens", C.c_int), ("hq", C.c_int),
+        ("hkv", C.c_int), ("head_dim", C.c_int), ("rot_dim", C.c_int),
+        ("num_pages", C.c_int), ("page_size", C.c_int),
+        ("max_pages", C.c_int), ("attn_factor", C.c_float),
+        ("status", C.c_void_p),
+    ]
+
+
+class AttnPagedParams(C.Structure):
+    """Mirror of tilemix_attn_paged_params (include/tilemix.h)."""
+    _fields_ = [
+        ("struct_size", C.c_uint32), ("dtype", C.c_int),
+        ("kv_format", C.c_int), ("causal", C.c_int),
+        ("q", C.c_void_p), ("q_stride_t", C.c_int64),
+        ("q_stride_h", C.c_int64),
+        ("k_pages", C.c_void_p), ("v_pages", C.c_void_p),
+        ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+        ("head_stride", C.c_int64),
+        ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+        ("page_table", C.c_void_p), ("table_stride", C.c_int64),
+        ("cu_seqlens", C.c_void_p), ("kv_lens", C.c_void_p),
+        ("batch", C.c_int), ("total_tokens", C.c_int),
+        ("max_q_len", C.c_int), ("max_kv_len", C.c_int),
+        ("hq", C.c_int), ("hkv", C.c_int), ("head_dim", C.c_int),
+        ("num_pages", C.c_int), ("page_size", C.c_int),
+        ("max_pages", C.c_int), ("softmax_scale", C.c_float),
+        ("out", C.c_void_p), ("lse", C.c_void_p), ("workspace", C.c_void_p),
+        ("workspace_bytes", C.c_size_t), ("status", C.c_void_p),
     ]
 
 
@@ -128,6 +210,18 @@ def _load() -> C.CDLL:
         vp, vp, vp]
     lib.tilemix_attn_prefill.restype = i32
     lib.tilemix_attn_prefill.argtypes = [C.POINTER(AttnParams), vp]
+    lib.tilemix_rope_frequencies.restype = i32
+    lib.tilemix_rope_frequencies.argtypes = [
+        i32, i32, C.c_double, C.c_double, C.c_double, C.c_double, i32,
+        C.POINTER(C.c_double), C.POINTER(C.c_float)]
+    lib.tilemix_rope.restype = i32
+    lib.tilemix_rope.argtypes = [C.POINTER(RopeParams), vp]
+    lib.tilemix_paged_append.restype = i32
+    lib.tilemix_paged_append.argtypes = [C.POINTER(AppendParams), vp]
+    lib.tilemix_attn_paged_workspace_bytes.restype = C.c_size_t
+    lib.tilemix_attn_paged_workspace_bytes.argtypes = [i32] * 4
+    lib.tilemix_attn_paged.restype = i32
+    lib.tilemix_attn_paged.argtypes = [C.POINTER(AttnPagedParams), vp]
     lib.tilemix_status_string.restype = C.c_char_p
     lib.tilemix_status_string.argtypes = [i32]
     lib.tilemix_last_error.restype = C.c_char_p
@@ -467,4 +561,329 @@ def tilemix_attn_prefill(q, k, v, cu_seqlens, max_seqlen: int, *, q8=None,
                                          _ptr(status))
     _check(lib.tilemix_attn_prefill(C.byref(p), _stream(stream)),
            "tilemix_attn_prefill")
+    return out
+
+
+# ----------------------------------------------------------------------------
+# rotary positions and the paged KV cache
+# ----------------------------------------------------------------------------
+
+class _On:
+    """The device and stream of a call: every tensor has to lie on the device
+    of the first one, which becomes current; without `stream` its current
+    stream is used.  Tensors made inside belong to that stream."""
+
+    def __init__(self, stream, **tensors):
+        torch = _torch()
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, not on {dev}")
+        self.device, self.handle = dev, stream.cuda_stream
+        self._stream = stream
+        self._ctx = None
+
+    def __enter__(self):
+        torch = _torch()
+        # entering the current stream again costs host time and does nothing
+        if (self.device.index != torch.cuda.current_device() or
+                self._stream != torch.cuda.current_stream()):
+            self._ctx = torch.cuda.stream(self._stream)
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _dtype_code(t, name):
+    torch = _torch()
+    if t.dtype == torch.float16:
+        return 0
+    if t.dtype == torch.bfloat16:
+        return 1
+    raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+
+
+def _rows(t, name, shape=None, dtype=None):
+    """Token and head strides of a [T, heads, d] tensor (an axis of one
+    counts as packed, whatever stride torch gives it)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    n, h, d = t.shape
+    if d > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    sh = t.stride(1) if h > 1 else d
+    return (t.stride(0) if n > 1 else h * sh), sh
+
+
+def _vector(t, name, n, dtype):
+    _dev(t, name, dtype)
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return t
+
+
+def _status_word(status):
+    """The caller's status word (int32, at least one element)."""
+    _dev(status, "status", _torch().int32)
+    if status is not None and status.numel() < 1:
+        raise ValueError("status must hold at least one element")
+
+
+def _layout_code(layout):
+    return ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+
+
+def _frequencies(freqs, head_dim):
+    """Rotated channels of a frequency vector."""
+    if freqs is None:
+        return 0
+    _dev(freqs, "freqs", _torch().float64)
+    if not 0 < 2 * freqs.numel() <= head_dim:
+        raise ValueError(f"freqs must have 1 .. head_dim / 2 elements, got "
+                         f"{freqs.numel()}")
+    return 2 * freqs.numel()
+
+
+def _set_cache(p, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
+               kv_lens, status, dtype):
+    """Checks the cache arguments and fills their fields of `p`."""
+    torch = _torch()
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, page_size, hkv, head_dim]")
+    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must share shape and dtype")
+    n, page, hkv, d = k_pages.shape
+    int8 = k_pages.dtype == torch.int8
+    if not int8 and k_pages.dtype != dtype:
+        raise ValueError(f"pages must be {dtype} or int8, got {k_pages.dtype}")
+    strides = []
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if d > 1 and t.stride(3) != 1:
+            raise ValueError(f"{name} must have contiguous channels")
+        th = t.stride(2) if hkv > 1 else d
+        tt = t.stride(1) if page > 1 else hkv * th
+        strides.append((t.stride(0) if n > 1 else page * tt, tt, th))
+    if strides[0] != strides[1]:
+        raise ValueError("k_pages and v_pages must share their strides")
+    if int8 != (k_scale is not None) or int8 != (v_scale is not None):
+        raise ValueError("k_scale and v_scale go with int8 pages, and only "
+                         "with them")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _dev(t, name, torch.float32)
+        if t is not None and tuple(t.shape) != (n, hkv, page):
+            raise ValueError(f"{name} must have shape {(n, hkv, page)}, got "
+                             f"{tuple(t.shape)}")
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have batch + 1 elements")
+    batch = cu_seqlens.numel() - 1
+    _dev(cu_seqlens, "cu_seqlens", torch.int32)
+    _vector(kv_lens, "kv_lens", batch, torch.int32)
+    if (page_table.dim() != 2 or page_table.shape[0] != batch or
+            page_table.dtype != torch.int32):
+        raise ValueError(f"page_table must be int32 [{batch}, max_pages]")
+    width = page_table.shape[1]
+    if width > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must have contiguous rows")
+    _status_word(status)
+    p.kv_format = KV_INT8 if int8 else KV_FP16
+    p.k_pages, p.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
+    p.page_stride, p.token_stride, p.head_stride = strides[0]
+    p.k_scale, p.v_scale = _ptr(k_scale), _ptr(v_scale)
+    p.page_table = page_table.data_ptr()
+    p.table_stride = page_table.stride(0) if batch > 1 else width
+    p.cu_seqlens, p.kv_lens = cu_seqlens.data_ptr(), kv_lens.data_ptr()
+    p.batch, p.num_pages, p.page_size, p.max_pages = batch, n, page, width
+    p.hkv, p.head_dim = hkv, d
+    p.status = _ptr(status)
+
+
+def tilemix_rope_frequencies(rot_dim: int, base: float = 10000.0, *,
+                             scaling: str = "none", factor: float = 1.0,
+                             low_freq_factor: float = 1.0,
+                             high_freq_factor: float = 4.0,
+                             original_max_position: int = 0, device=None):
+    """Rotary frequencies (radians per position) as a float64 tensor
+    [rot_dim / 2] on `device` (host without one), and the attn_factor that
+    goes with them.  `scaling`: one of ROPE_SCALINGS; "yarn" takes its two
+    rotation counts (32 and 1 usually) as high_freq_factor and
+    low_freq_factor."""
+    torch = _torch()
+    code = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    buf = (C.c_double * max(1, rot_dim // 2))()
+    att = C.c_float(1.0)
+    _check(lib.tilemix_rope_frequencies(
+        code, rot_dim, base, factor, low_freq_factor, high_freq_factor,
+        original_max_position, buf, C.byref(att)), "tilemix_rope_frequencies")
+    freqs = torch.tensor(list(buf), dtype=torch.float64, device=device)
+    return freqs, float(att.value)
+
+
+def tilemix_rope(q, k, positions, freqs, *, layout="half",
+                 attn_factor: float = 1.0, inverse: bool = False, q_out=None,
+                 k_out=None, stream=None):
+    """Rotary positions of q [T, hq, d] and k [T, hkv, d] (k may be None) in
+    one launch; fp16 or bf16, token and head strides free.  positions int32
+    [T], freqs float64 [rot_dim / 2] on the device (channels past rot_dim are
+    copied).  `inverse` rotates back, which is also the gradient.  Outputs
+    default to new contiguous tensors; q_out=q rotates in place.
+    Returns (q_out, k_out)."""
+    torch = _torch()
+    with _On(stream, q=q, k=k, positions=positions, freqs=freqs, q_out=q_out,
+             k_out=k_out) as on:
+        p = RopeParams()
+        p.struct_size = C.sizeof(RopeParams)
+        p.dtype = _dtype_code(q, "q")
+        p.q_stride_t, p.q_stride_h = _rows(q, "q")
+        t, hq, d = q.shape
+        _vector(positions, "positions", t, torch.int32)
+        p.rot_dim = _frequencies(freqs, d)
+        if q_out is None:
+            q_out = torch.empty((t, hq, d), dtype=q.dtype, device=on.device)
+        p.q_out_stride_t, p.q_out_stride_h = _rows(q_out, "q_out", q.shape,
+                                                   q.dtype)
+        if k is not None:
+            if k.dim() != 3 or k.shape[0] != t or k.shape[2] != d:
+                raise ValueError("q and k must share tokens and head_dim")
+            p.k_stride_t, p.k_stride_h = _rows(k, "k", None, q.dtype)
+            p.hkv = k.shape[1]
+            if k_out is None:
+                k_out = torch.empty(tuple(k.shape), dtype=q.dtype,
+                                    device=on.device)
+            p.k_out_stride_t, p.k_out_stride_h = _rows(k_out, "k_out", k.shape,
+                                                       q.dtype)
+            p.k, p.k_out = k.data_ptr(), k_out.data_ptr()
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        p.layout, p.inverse = _layout_code(layout), int(bool(inverse))
+        p.q, p.q_out = q.data_ptr(), q_out.data_ptr()
+        p.positions, p.freqs = positions.data_ptr(), freqs.data_ptr()
+        p.attn_factor = attn_factor
+        p.total_tokens, p.hq, p.head_dim = t, hq, d
+        _check(lib.tilemix_rope(C.byref(p), on.handle), "tilemix_rope")
+    return q_out, k_out
+
+
+def tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
+                         v_pages, *, k_scale=None, v_scale=None, q=None,
+                         q_out=None, positions=None, freqs=None,
+                         layout="half", attn_factor: float = 1.0, status=None,
+                         stream=None):
+    """Writes the new tokens' k and v [T, hkv, d] into the pages of the cache
+    in one launch: token i of sequence b (n_b of them) to position kv_lens[b]
+    - n_b + i.  k_pages, v_pages [num_pages, page_size, hkv, d] of the same
+    type, or int8 with k_scale, v_scale fp32 [num_pages, hkv, page_size].
+    With freqs, k (and q, if given) is rotated on the way, by each token's
+    position in the cache or by `positions`.  Returns the rotated q (rows
+    past cu_seqlens[-1] are not written) or None."""
+    torch = _torch()
+    with _On(stream, k=k, v=v, page_table=page_table, cu_seqlens=cu_seqlens,
+             kv_lens=kv_lens, k_pages=k_pages, v_pages=v_pages,
+             k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
+             positions=positions, freqs=freqs, status=status) as on:
+        p = AppendParams()
+        p.struct_size = C.sizeof(AppendParams)
+        p.dtype = _dtype_code(k, "k")
+        _set_cache(p, k_pages, v_pages, k_scale, v_scale, page_table,
+                   cu_seqlens, kv_lens, status, k.dtype)
+        p.k_stride_t, p.k_stride_h = _rows(k, "k")
+        t, hkv, d = k.shape
+        if (hkv, d) != (p.hkv, p.head_dim):
+            raise ValueError("k and the pages must share heads and head_dim")
+        p.v_stride_t, p.v_stride_h = _rows(v, "v", k.shape, k.dtype)
+        p.rot_dim = _frequencies(freqs, d)
+        if freqs is None and (q is not None or positions is not None):
+            raise ValueError("q and positions need freqs")
+        if positions is not None:
+            _vector(positions, "positions", t, torch.int32)
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != t or q.shape[2] != d:
+                raise ValueError("q and k must share tokens and head_dim")
+            p.q_stride_t, p.q_stride_h = _rows(q, "q", None, k.dtype)
+            if q_out is None:
+                q_out = torch.empty(tuple(q.shape), dtype=k.dtype,
+                                    device=on.device)
+            p.q_out_stride_t, p.q_out_stride_h = _rows(q_out, "q_out", q.shape,
+                                                       k.dtype)
+            p.hq, p.q, p.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        p.layout = _layout_code(layout)
+        p.k, p.v = k.data_ptr(), v.data_ptr()
+        p.positions, p.freqs = _ptr(positions), _ptr(freqs)
+        p.attn_factor, p.total_tokens = attn_factor, t
+        _check(lib.tilemix_paged_append(C.byref(p), on.handle),
+               "tilemix_paged_append")
+    return q_out
+
+
+def tilemix_attn_paged_workspace_bytes(max_q_len: int, hq: int, hkv: int,
+                                       head_dim: int) -> int:
+    """Bytes of device scratch tilemix_attn_paged needs."""
+    return int(lib.tilemix_attn_paged_workspace_bytes(max_q_len, hq, hkv,
+                                                      head_dim))
+
+
+def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
+                       max_q_len: int, max_kv_len: int, *, k_scale=None,
+                       v_scale=None, causal: bool = True,
+                       softmax_scale: float = 0.0, out=None, lse=None,
+                       workspace=None, status=None, stream=None):
+    """Attention of the new tokens q [T, hq, d] (fp16 or bf16) over the paged
+    cache: kv_lens int32 [B] counts each sequence's keys, the new tokens' own
+    among them when `causal`.  max_q_len and max_kv_len bound the sequences'
+    new tokens and keys.  `workspace` (a CUDA tensor, 16-byte aligned, of
+    tilemix_attn_paged_workspace_bytes) is allocated here when not given; two
+    calls that may run at the same time need two.  Rows of q past
+    cu_seqlens[-1] are neither read nor written.  Returns out [T, hq, d]."""
+    torch = _torch()
+    with _On(stream, q=q, k_pages=k_pages, v_pages=v_pages,
+             page_table=page_table, cu_seqlens=cu_seqlens, kv_lens=kv_lens,
+             k_scale=k_scale, v_scale=v_scale, out=out, lse=lse,
+             workspace=workspace, status=status) as on:
+        p = AttnPagedParams()
+        p.struct_size = C.sizeof(AttnPagedParams)
+        p.dtype = _dtype_code(q, "q")
+        _set_cache(p, k_pages, v_pages, k_scale, v_scale, page_table,
+                   cu_seqlens, kv_lens, status, q.dtype)
+        p.q_stride_t, p.q_stride_h = _rows(q, "q")
+        t, hq, d = q.shape
+        if d != p.head_dim:
+            raise ValueError("q and the pages must share head_dim")
+        if out is None:
+            out = torch.empty((t, hq, d), dtype=q.dtype, device=on.device)
+        _dev(out, "out", q.dtype)
+        if tuple(out.shape) != (t, hq, d):
+            raise ValueError(f"out must have shape {(t, hq, d)}")
+        _vector(lse, "lse", hq * t, torch.float32)
+        if workspace is None:
+            need = tilemix_attn_paged_workspace_bytes(max_q_len, hq, p.hkv, d)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8,
+                                    device=on.device)
+        _dev(workspace, "workspace")
+        p.q, p.out, p.lse = q.data_ptr(), out.data_ptr(), _ptr(lse)
+        p.workspace = workspace.data_ptr()
+        p.workspace_bytes = workspace.numel() * workspace.element_size()
+        p.causal, p.softmax_scale = int(bool(causal)), softmax_scale
+        p.total_tokens, p.hq = t, hq
+        p.max_q_len, p.max_kv_len = max_q_len, max_kv_len
+        _check(lib.tilemix_attn_paged(C.byref(p), on.handle),
+               "tilemix_attn_paged")
     return out

@@ -1,0 +1,798 @@
+// Attention of few new tokens over a paged KV cache (decoded tokens, drafted
+// ones; any other call too, at the cost of reading the cache once per 16
+// packed rows).
+//
+// Mathematics.  The query heads of one KV head and the new tokens pack into
+// rows (row = token * group + head), so a KV head's keys are read once for
+// all of them.  Per row: running maximum m (base-2 logits), sum l and
+// unnormalised output O, merged over key ranges by
+//   m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), O likewise.
+// O is rescaled lazily: m only moves when a key exceeds it by more than 2^8,
+// so P <= 2^8 fits fp16.  l adds P before it is rounded for the product, so
+// lse keeps fp32 accuracy.
+// INT8 pages: K codes convert exactly to the query's 16-bit type and their
+// scale multiplies the fp32 score.  V codes convert exactly to fp16; their
+// scale joins P, which is then P sv 2^-E with 2^E the (lazily raised) power
+// of two above the scales seen, so that small scales do not fall into fp16
+// subnormals and large ones do not overflow.
+//
+// Work split.  All keys of all (sequence, KV head, 16-row tile) items, in
+// units of 64 keys, form one line; block c takes the c-th equal part of it.
+// An item that one block holds whole is written out; the others leave partial
+// results that the merge kernel adds in key order.  No block waits for
+// another, and the split follows from the lengths alone.
+//
+// What bounds it: HBM.  Each warp owns every fourth 16-key group of a block's
+// part and runs alone (private m, l, O and a private ring of TMA slots, no
+// block barrier in the loop), so a block keeps 4 rings of loads in flight.
+// The products are small (two m16n8k16 per key for d = 128, a fifth of the
+// tensor rate at full HBM speed), hence warp-level mma fragments that never
+// leave registers.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
+#include "paged_common.cuh"
+#include "ptx.cuh"
+
+namespace tilemix {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;    // packed rows of an item (mma M)
+constexpr int kGroup = 16;   // keys of a ring slot
+constexpr int kUnit = kWarps * kGroup;  // keys of a unit of work
+constexpr int kBlocksPerSm = 2;
+constexpr int kGridMax = 148 * kBlocksPerSm;
+
+template <int D, bool INT8>
+struct Cfg {
+  static constexpr int kElem = INT8 ? 1 : 2;
+  static constexpr int kTile = kGroup * D * kElem;  // K or V bytes of a slot
+  static constexpr int kScale = INT8 ? 2 * kGroup * 4 : 0;
+  static constexpr int kSlot = 2 * kTile;
+  // 24 KB of ring per warp, at most 8 slots
+  static constexpr int kSlots = 24576 / kSlot > 8 ? 8 : 24576 / kSlot;
+  static constexpr int kRing = kSlots * kSlot;
+  static constexpr int kRingAll = kWarps * kRing;
+  static constexpr int kScaleOff = kRingAll;
+  static constexpr int kScaleAll = kWarps * kSlots * kScale;
+  static constexpr int kBarOff = kScaleOff + kScaleAll;
+  static constexpr int kSmem = kBarOff + kWarps * kSlots * 8 + 1024;
+  // 16 rows of O, and m, l, merged through the warp's own ring
+  static constexpr int kMergeStride = D + 4;
+  static_assert(kRows * kMergeStride * 4 <= kRing, "merge area");
+};
+
+__device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr));
+}
+
+__device__ __forceinline__ void ldm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr));
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4],
+                                         uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return pack_half2(lo, hi);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// Four int8 codes -> two bf16 pairs, exactly: |low 7 bits| under the bf16
+// exponent of 128 minus 128 or, for a set sign bit, minus 256.
+__device__ __forceinline__ void i8x4_to_bf2x2(uint32_t w, uint32_t& lo,
+                                              uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0u, 0x4140), b = __byte_perm(w, 0u, 0x4342);
+  const uint32_t am = (a & 0x007f007fu) | 0x43004300u;
+  const uint32_t as = (a & 0x00800080u) | 0x43004300u;
+  const uint32_t bm = (b & 0x007f007fu) | 0x43004300u;
+  const uint32_t bs = (b & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 x =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&am),
+              *reinterpret_cast<const __nv_bfloat162*>(&as));
+  const __nv_bfloat162 y =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&bm),
+              *reinterpret_cast<const __nv_bfloat162*>(&bs));
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// Position of a unit of work.
+struct Cursor {
+  int b, kvh, qt;
+  int unit;  // unit inside the item
+};
+
+__device__ __forceinline__ int item_units(const PagedArgs& p, const SeqGeom& g,
+                                          int qt) {
+  // keys of the tile's last row
+  const int rows = g.n * p.group;
+  const int last = min((qt + 1) * kRows, rows) - 1;
+  const int keys = keys_of_token(p, g, last / p.group);
+  return max(1, (keys + kUnit - 1) / kUnit);
+}
+
+__device__ __forceinline__ int tiles_of(const PagedArgs& p, const SeqGeom& g) {
+  return (g.n * p.group + kRows - 1) / kRows;
+}
+
+__device__ __forceinline__ long long head_units(const PagedArgs& p,
+                                                const SeqGeom& g) {
+  long long s = 0;
+  const int tiles = tiles_of(p, g);
+  for (int qt = 0; qt < tiles; ++qt) s += item_units(p, g, qt);
+  return s;
+}
+
+// Total units, by all lanes of a warp.
+__device__ __forceinline__ long long total_units(const PagedArgs& p, int lane,
+                                                 bool report) {
+  long long s = 0;
+  for (int b = lane; b < p.batch; b += 32)
+    s += head_units(p, seq_geom(p, b, report)) * p.hkv;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// The item and unit at position w of the line (w < total).
+__device__ __forceinline__ Cursor locate(const PagedArgs& p, long long w,
+                                         int lane) {
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    long long mine = 0, per_head = 0;
+    if (b < p.batch) {
+      per_head = head_units(p, seq_geom(p, b, false));
+      mine = per_head * p.hkv;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, incl > w);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const long long before = __shfl_sync(0xffffffffu, incl - mine, l);
+      const long long ph = __shfl_sync(0xffffffffu, per_head, l);
+      Cursor c;
+      c.b = b0 + l;
+      long long rem = w - before;
+      c.kvh = static_cast<int>(rem / ph);
+      rem -= c.kvh * ph;
+      const SeqGeom g = seq_geom(p, c.b, false);
+      c.qt = 0;
+      while (true) {
+        const int u = item_units(p, g, c.qt);
+        if (rem < u) break;
+        rem -= u;
+        ++c.qt;
+      }
+      c.unit = static_cast<int>(rem);
+      return c;
+    }
+    w -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return Cursor{0, 0, 0, 0};  // not reached for w < total
+}
+
+// Partial-result slots: 2 c for an item that began in an earlier block, 2 c
+// + 1 for one that begins in block c and goes on.  Header {used, ends here,
+// bad, rows}; second word of slot 2 c + 1's item: {b, kvh, qt, -}.
+template <int D>
+__device__ __forceinline__ float* part_rows(const PagedArgs& p, int slot) {
+  return p.part + static_cast<size_t>(slot) * kRows * (D + 2);
+}
+
+template <int D, bool BF16, bool INT8>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    step_kernel(const __grid_constant__ PagedArgs p) {
+  using C = Cfg<D, INT8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g8 = lane >> 2, q4 = lane & 3;  // fragment row, quad column
+  uint8_t* ring = smem + warp * C::kRing;
+  const uint32_t ring_a = smem_u32(ring);
+  uint8_t* scales = smem + C::kScaleOff + warp * C::kSlots * C::kScale;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * C::kSlots;
+  __shared__ int s_bad;
+  if (lane == 0) {
+    for (int s = 0; s < C::kSlots; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+
+  const long long total = total_units(p, lane, blockIdx.x == 0 && warp == 0);
+  const long long w0 = total * blockIdx.x / gridDim.x;
+  const long long w1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (threadIdx.x < 2)
+    p.head[4 * blockIdx.x + 2 * threadIdx.x] = make_int4(0, 0, 0, 0);
+  if (w0 >= w1) return;
+  Cursor cur = locate(p, w0, lane);
+  long long left = w1 - w0;
+  uint32_t issued = 0, consumed = 0;  // ring slots, over all items
+  bool dead = false;                  // a wait ran out
+
+  while (left > 0) {
+    const SeqGeom g = seq_geom(p, cur.b, false);
+    const int units = item_units(p, g, cur.qt);
+    const int ua = cur.unit;
+    const int ub = static_cast<int>(min(static_cast<long long>(units), ua + left));
+    const int row0 = cur.qt * kRows;
+    const int nrows = min(kRows, g.n * p.group - row0);
+    const int tok_first = row0 / p.group;
+    const int tok_last = (row0 + nrows - 1) / p.group;
+    const int keys = keys_of_token(p, g, tok_last);     // the tile's limit
+    const int keys_min = keys_of_token(p, g, tok_first);  // its first row's
+    // rows of this thread: g8 and g8 + 8
+    int lim[2];
+    const uint16_t* qrow[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g8 + 8 * i;
+      const int pr = row0 + min(r, nrows - 1);
+      const int tok = pr / p.group;
+      lim[i] = r < nrows ? keys_of_token(p, g, tok) : 0;
+      qrow[i] = r < nrows ? p.q + static_cast<int64_t>(g.start + tok) * p.q_st +
+                                static_cast<int64_t>(cur.kvh * p.group +
+                                                     pr % p.group) * p.q_sh
+                          : nullptr;
+    }
+
+    // this warp's 16-key groups of units [ua, ub): i-th at key k0 + 64 i
+    const int k0 = ua * kUnit + warp * kGroup;
+    const int kend = min(keys, ub * kUnit);
+    const int nst = dead || k0 >= kend ? 0 : (kend - k0 + kUnit - 1) / kUnit;
+    const int32_t* trow = p.page_table + cur.b * p.table_stride;
+    int pid = 0, pid_base = -32;
+    bool bad_page = false;
+    auto fetch_pids = [&](int base) {
+      pid_base = base;
+      const int i = base + lane;
+      pid = 0;
+      if (i < nst) {
+        pid = trow[(k0 + static_cast<long long>(i) * kUnit) >> p.page_shift];
+        if (pid < 0 || pid >= p.num_pages) {
+          bad_page = true;
+          report_status(p.status, kStatusBadPages);
+          pid = 0;
+        }
+      }
+    };
+    auto issue = [&](int i) {
+      if (i - pid_base >= 32) fetch_pids(i);
+      const int id = __shfl_sync(0xffffffffu, pid, i - pid_base);
+      const uint32_t s = issued % C::kSlots;
+      if (lane == 0) {
+        const int slot = (k0 + i * kUnit) & ((1 << p.page_shift) - 1);
+        uint8_t* dst = ring + s * C::kSlot;
+        mbar_arrive_expect_tx(&bars[s], C::kSlot + C::kScale);
+        if (INT8) {
+          tma_load_4d(dst, &p.tm_k, &bars[s], 0, slot, cur.kvh, id);
+          tma_load_4d(dst + C::kTile, &p.tm_v, &bars[s], 0, slot, cur.kvh, id);
+          const int64_t at =
+              ((static_cast<int64_t>(id) * p.hkv + cur.kvh) << p.page_shift) + slot;
+          bulk_load(scales + s * C::kScale, p.k_scale + at, kGroup * 4, &bars[s]);
+          bulk_load(scales + s * C::kScale + kGroup * 4, p.v_scale + at,
+                    kGroup * 4, &bars[s]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(dst + c * kGroup * 128, &p.tm_k, &bars[s], c * 64, slot,
+                        cur.kvh, id);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(dst + C::kTile + c * kGroup * 128, &p.tm_v, &bars[s],
+                        c * 64, slot, cur.kvh, id);
+        }
+      }
+      ++issued;
+    };
+    if (nst > 0) fetch_pids(0);
+    int next = 0;
+    for (; next < C::kSlots && next < nst; ++next) issue(next);
+
+    // Q fragments of the whole tile.  INT8: the contraction runs over the
+    // channels in the order 64 j + 16 q + 4 s + e (quad q, k-step 4 j + s),
+    // so that a thread's codes of four k-steps are 16 consecutive bytes.
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const int c0 = INT8 ? 64 * (s >> 2) + 16 * q4 + 4 * (s & 3) : 16 * s + 2 * q4;
+      const int c1 = INT8 ? c0 + 2 : c0 + 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        qf[s][i] = qrow[i] ? *reinterpret_cast<const uint32_t*>(qrow[i] + c0) : 0u;
+        qf[s][2 + i] =
+            qrow[i] ? *reinterpret_cast<const uint32_t*>(qrow[i] + c1) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F};  // running max (base 2)
+    float l[2] = {0.0f, 0.0f};                    // this thread's sums
+    float inv = 0.0f;  // INT8: 2^-E of the V scales (0: none seen)
+
+    for (int i = 0; i < nst; ++i) {
+      const uint32_t s = consumed % C::kSlots;
+      const bool got = mbar_wait(&bars[s], (consumed / C::kSlots) & 1, nullptr);
+      if (!__all_sync(0xffffffffu, got)) {
+        report_status(p.status, kStatusTimeout);
+        dead = true;
+        break;
+      }
+      ++consumed;
+      const uint32_t ka = ring_a + s * C::kSlot;
+      const uint32_t va = ka + C::kTile;
+      const int key0 = k0 + i * kUnit;
+      float sc[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[j][e] = 0.0f;
+      // keys of columns 2 q4 and 2 q4 + 1 of fragment j: key0 + kc[j][.]
+      // (INT8 rows are taken in the order 0, 4, 1, 5, 2, 6, 3, 7, which
+      // spreads a quarter warp's 16-byte reads over all banks)
+      const int ca = INT8 ? q4 : 2 * q4, cb = INT8 ? q4 + 4 : 2 * q4 + 1;
+      float skv[4], svv[4];
+      if (INT8) {
+        const uint32_t sa = smem_u32(scales + s * C::kScale);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          skv[2 * j] = __uint_as_float(lds32(sa + (8 * j + ca) * 4));
+          skv[2 * j + 1] = __uint_as_float(lds32(sa + (8 * j + cb) * 4));
+          svv[2 * j] = __uint_as_float(lds32(sa + kGroup * 4 + (8 * j + ca) * 4));
+          svv[2 * j + 1] =
+              __uint_as_float(lds32(sa + kGroup * 4 + (8 * j + cb) * 4));
+        }
+        const int kr = (g8 >> 1) | ((g8 & 1) << 2);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t off = (8 * j + kr) * D + 64 * c + 16 * q4;
+            const uint4 w = lds128(ka + swz(off, D == 128 ? 7u : 3u));
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              uint32_t b0, b1;
+              if (BF16) i8x4_to_bf2x2(ws[t], b0, b1);
+              else i8x4_to_h2x2(ws[t], b0, b1);
+              mma16816<BF16>(sc[j], qf[4 * c + t], b0, b1);
+            }
+          }
+      } else {
+        // lanes 0-7 keys 0-7 low channels, 8-15 the same keys' high
+        // channels, 16-31 keys 8-15
+        const int kr = (lane & 7) + ((lane >> 4) << 3);
+        const int hi = (lane >> 3) & 1;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+          const uint32_t off =
+              (t >> 2) * kGroup * 128 + kr * 128 + (t & 3) * 32 + hi * 16;
+          uint32_t b[4];
+          ldm_x4(ka + swz(off, 7u), b);
+          mma16816<BF16>(sc[0], qf[t], b[0], b[1]);
+          mma16816<BF16>(sc[1], qf[t], b[2], b[3]);
+        }
+      }
+      // scores in base-2 logits; masked ones -inf (by position, whatever the
+      // slot held)
+      const bool masked = key0 + kGroup > keys_min;
+      float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = sc[j][e] * p.scale_log2;
+          if (INT8) x *= skv[2 * j + (e & 1)];
+          if (masked && key0 + 8 * j + ((e & 1) ? cb : ca) >= lim[e >> 1])
+            x = -CUDART_INF_F;
+          sc[j][e] = x;
+          mx[e >> 1] = fmaxf(mx[e >> 1], x);
+        }
+      bool grow = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        grow |= mx[r] > m[r] + kRescaleThreshold;
+      }
+      float svm = 0.0f;
+      if (INT8) {
+        // slots past the sequence's end may hold anything
+        const int live = g.len - key0;
+        svm = fmaxf(fmaxf(ca < live ? svv[0] : 0.0f, cb < live ? svv[1] : 0.0f),
+                    fmaxf(8 + ca < live ? svv[2] : 0.0f,
+                          8 + cb < live ? svv[3] : 0.0f));
+        svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, 1));
+        svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, 2));
+        grow |= inv == 0.0f ? svm > 0.0f : svm * inv > 32.0f;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        float f = 1.0f;
+        if (INT8 && svm > 0.0f && (inv == 0.0f || svm * inv > 32.0f)) {
+          const int e = min(max(ilogbf(svm) + 1, -126), 126);
+          const float ninv = ldexpf(1.0f, -e);
+          f = inv == 0.0f ? 0.0f : ninv / inv;
+          inv = ninv;
+        }
+        float al[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          al[r] = 1.0f;
+          if (mx[r] > m[r] + kRescaleThreshold) {
+            al[r] = ex2_approx(m[r] - mx[r]);
+            m[r] = mx[r];
+          }
+          l[r] *= al[r];
+          al[r] *= f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][0] *= al[0];
+          o[j][1] *= al[0];
+          o[j][2] *= al[1];
+          o[j][3] *= al[1];
+        }
+      }
+      // P; a row that has seen no key keeps m = -inf and P = 0
+      const float mu[2] = {m[0] == -CUDART_INF_F ? 0.0f : m[0],
+                           m[1] == -CUDART_INF_F ? 0.0f : m[1]};
+      uint32_t pf[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float e4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          e4[e] = ex2_approx(sc[j][e] - mu[e >> 1]);
+          l[e >> 1] += e4[e];
+          if (INT8) {
+            const int key = 8 * j + ((e & 1) ? cb : ca);
+            // P = 0 times the scale of a slot past the end must stay 0
+            e4[e] = key0 + key < g.len ? e4[e] * (svv[2 * j + (e & 1)] * inv) : 0.0f;
+          }
+        }
+        pf[2 * j] = pack2<BF16 && !INT8>(e4[0], e4[1]);
+        pf[2 * j + 1] = pack2<BF16 && !INT8>(e4[2], e4[3]);
+      }
+      // V rows past the sequence's end may hold NaN: cleared in registers
+      const bool tail = key0 + kGroup > g.len;
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+      if (INT8) {
+        // any int8 code is finite: P = 0 is enough
+        // ldmatrix rows in the order of the score columns: row 2q -> q, ...
+        const int r8 = lane & 7;
+        const int kr = ((r8 >> 1) | ((r8 & 1) << 2)) + ((lane >> 3) & 1) * 8;
+        const int hi = lane >> 4;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t b[4];
+          ldm_x4_t(va + swz(kr * D + c * 32 + hi * 16, D == 128 ? 7u : 3u), b);
+          // b[0], b[1]: keys 0-7, 8-15 of 16 channels; b[2], b[3]: the next 16
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = b[2 * h] ^ 0x80808080u, y = b[2 * h + 1] ^ 0x80808080u;
+            const __half2 bias = __float2half2_rn(1152.0f);
+            uint32_t xe = __byte_perm(x, 0x64646464u, 0x4240);
+            uint32_t xo = __byte_perm(x, 0x64646464u, 0x4341);
+            uint32_t ye = __byte_perm(y, 0x64646464u, 0x4240);
+            uint32_t yo = __byte_perm(y, 0x64646464u, 0x4341);
+            auto sub = [&](uint32_t& z) {
+              const __half2 t = __hsub2(*reinterpret_cast<__half2*>(&z), bias);
+              z = *reinterpret_cast<const uint32_t*>(&t);
+            };
+            sub(xe);
+            sub(xo);
+            sub(ye);
+            sub(yo);
+            // even and odd channels of the 16 as two n-tiles
+            mma16816<false>(o[4 * c + 2 * h], pf, xe, ye);
+            mma16816<false>(o[4 * c + 2 * h + 1], pf, xo, yo);
+          }
+        }
+      } else {
+        if (tail) {
+          const int live = g.len - key0;  // keys 2 q4, + 1, + 8, + 9
+          auto keep = [&](int k) {
+            return (k < live ? 0x0000ffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
+          };
+          keep0 = keep(2 * q4);
+          keep1 = keep(2 * q4 + 8);
+        }
+        const int kr = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const int hi = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+          const uint32_t off =
+              (t >> 2) * kGroup * 128 + kr * 128 + (t & 3) * 32 + hi * 16;
+          uint32_t b[4];
+          ldm_x4_t(va + swz(off, 7u), b);
+          if (tail) {
+            b[0] &= keep0;
+            b[1] &= keep1;
+            b[2] &= keep0;
+            b[3] &= keep1;
+          }
+          mma16816<BF16>(o[2 * t], pf, b[0], b[1]);
+          mma16816<BF16>(o[2 * t + 1], pf, b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (next < nst) {
+        issue(next);
+        ++next;
+      }
+    }
+    if (dead) {  // let the copies in flight land (bounded), read nothing
+      for (; consumed < issued; ++consumed)
+        mbar_wait(&bars[consumed % C::kSlots], (consumed / C::kSlots) & 1, nullptr);
+    }
+    const bool any_bad = __any_sync(0xffffffffu, bad_page) || dead;
+
+    // ---- the four warps' results merge through their own rings ----
+    float* mine = reinterpret_cast<float*>(ring);
+    if (INT8) {  // back to the scale of V
+      const float e = inv > 0.0f ? 1.0f / inv : 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[j][k] *= e;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      float* row = mine + (g8 + 8 * r) * C::kMergeStride;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        if (INT8) {
+          // tiles 2 j', 2 j' + 1: channels 16 j' + 4 q4 + {0, 2} and {1, 3}
+          const int c = 16 * (j >> 1) + 4 * q4 + (j & 1);
+          row[c] = o[j][2 * r];
+          row[c + 2] = o[j][2 * r + 1];
+        } else {
+          *reinterpret_cast<float2*>(row + 8 * j + 2 * q4) =
+              make_float2(o[j][2 * r], o[j][2 * r + 1]);
+        }
+      }
+      if (q4 == 0) {
+        row[D] = m[r];
+        row[D + 1] = l[r];
+      }
+    }
+    if (any_bad && lane == 0) s_bad = 1;
+    __syncthreads();
+    const bool bad = s_bad != 0;
+    const bool whole = ua == 0 && ub == units;
+    const int slot = 2 * blockIdx.x + (ua == 0 ? 1 : 0);
+    // thread: row threadIdx / 8, channels 4 (threadIdx % 8) + 32 k
+    {
+      const int r = threadIdx.x >> 3, c8 = threadIdx.x & 7;
+      float mw[kWarps], mt = -CUDART_INF_F;
+      const float* rows[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        rows[w] = reinterpret_cast<const float*>(smem + w * C::kRing) +
+                  r * C::kMergeStride;
+        mw[w] = rows[w][D];
+        mt = fmaxf(mt, mw[w]);
+      }
+      float f[kWarps], lt = 0.0f;
+      const float mz = mt == -CUDART_INF_F ? 0.0f : mt;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        f[w] = ex2_approx(mw[w] - mz);
+        lt += f[w] * rows[w][D + 1];
+      }
+      if (r < nrows && !(whole && bad)) {
+        const int pr = row0 + r;
+        const int tok = g.start + pr / p.group;
+        const int h = cur.kvh * p.group + pr % p.group;
+        const float il = lt == 0.0f ? 0.0f : 1.0f / lt;
+        uint16_t* dst = p.out + (static_cast<int64_t>(tok) * p.hq + h) * D;
+        float* prow = part_rows<D>(p, slot) + r * (D + 2);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const int c = 4 * c8 + 32 * k;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(rows[w] + c);
+            a.x += f[w] * v.x;
+            a.y += f[w] * v.y;
+            a.z += f[w] * v.z;
+            a.w += f[w] * v.w;
+          }
+          if (whole) {
+            *reinterpret_cast<uint2*>(dst + c) = make_uint2(
+                pack2<BF16>(a.x * il, a.y * il), pack2<BF16>(a.z * il, a.w * il));
+          } else {
+            *reinterpret_cast<float2*>(prow + c) = make_float2(a.x, a.y);
+            *reinterpret_cast<float2*>(prow + c + 2) = make_float2(a.z, a.w);
+          }
+        }
+        if (c8 == 0) {
+          if (whole) {
+            if (p.lse)
+              p.lse[static_cast<int64_t>(h) * p.total_tokens + tok] =
+                  lt != 0.0f ? (mt + log2f(lt)) * 0.69314718055994530942f
+                            : -CUDART_INF_F;
+          } else {
+            prow[D] = mt;
+            prow[D + 1] = lt;
+          }
+        }
+      }
+    }
+    if (!whole && threadIdx.x == 0) {
+      p.head[2 * slot] = make_int4(1, ub == units ? 1 : 0, bad ? 1 : 0, nrows);
+      p.head[2 * slot + 1] = make_int4(cur.b, cur.kvh, cur.qt, g.start);
+    }
+    // the rings take TMA writes again: order the generic accesses before
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+
+    left -= ub - ua;
+    cur.unit = 0;
+    if (left > 0) {  // next item (sequences without rows have none)
+      if (++cur.qt >= tiles_of(p, g)) {
+        cur.qt = 0;
+        if (++cur.kvh >= p.hkv) {
+          cur.kvh = 0;
+          do {
+            ++cur.b;
+          } while (cur.b < p.batch - 1 && seq_geom(p, cur.b, false).n == 0);
+        }
+      }
+    }
+  }
+}
+
+// Adds the partial results of the item that begins in block blockIdx.x and
+// goes on in the next ones, row blockIdx.y, in key order.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(D)
+    merge_kernel(const __grid_constant__ PagedArgs p, int blocks) {
+  const int c = blockIdx.x;
+  const int slot = 2 * c + 1;
+  const int4 h = p.head[2 * slot];
+  const int r = blockIdx.y;
+  if (!h.x || r >= h.w) return;
+  const int4 it = p.head[2 * slot + 1];
+  const int ch = threadIdx.x;
+  const float* a = part_rows<D>(p, slot) + r * (D + 2);
+  float m = a[D], l = a[D + 1], o = a[ch];
+  bool bad = h.z != 0, done = false;
+  for (int b = c + 1; b < blocks && !done; ++b) {
+    const int4 n = p.head[4 * b];
+    if (!n.x) continue;  // a block without work
+    bad |= n.z != 0;
+    done = n.y != 0;
+    const float* x = part_rows<D>(p, 2 * b) + r * (D + 2);
+    const float mb = x[D], mn = fmaxf(m, mb);
+    const float mz = mn == -CUDART_INF_F ? 0.0f : mn;
+    const float fa = ex2_approx(m - mz), fb = ex2_approx(mb - mz);
+    o = o * fa + x[ch] * fb;
+    l = l * fa + x[D + 1] * fb;
+    m = mn;
+  }
+  if (bad || !done) return;
+  const int pr = it.z * kRows + r;
+  const int tok = it.w + pr / p.group;
+  const int hq = it.y * p.group + pr % p.group;
+  const float v = l == 0.0f ? 0.0f : o / l;
+  const int64_t at = (static_cast<int64_t>(tok) * p.hq + hq) * D + ch;
+  if (BF16) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    p.out[at] = *reinterpret_cast<const uint16_t*>(&b);
+  } else {
+    p.out[at] = __half_as_ushort(__float2half_rn(v));
+  }
+  if (p.lse && ch == 0)
+    p.lse[static_cast<int64_t>(hq) * p.total_tokens + tok] =
+        l != 0.0f ? (m + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
+}
+
+template <int D, bool BF16, bool INT8>
+cudaError_t launch_one(PagedArgs a, cudaStream_t stream) {
+  using C = Cfg<D, INT8>;
+  auto kern = step_kernel<D, BF16, INT8>;
+  cudaError_t e = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<kGridMax, kThreads, C::kSmem, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int rows = static_cast<int>(
+      min(static_cast<long long>(kRows),
+          static_cast<long long>(a.max_q_len) * a.group));
+  merge_kernel<D, BF16><<<dim3(kGridMax, rows), D, 0, stream>>>(a, kGridMax);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs& a, const PagedShape& s,
+                     cudaStream_t stream) {
+  if (s.int8)
+    return s.bf16 ? launch_one<D, true, true>(a, stream)
+                  : launch_one<D, false, true>(a, stream);
+  return s.bf16 ? launch_one<D, true, false>(a, stream)
+                : launch_one<D, false, false>(a, stream);
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(int head_dim) {
+  return static_cast<size_t>(2 * kGridMax) *
+         (kRows * (head_dim + 2) * sizeof(float) + 2 * sizeof(int4));
+}
+
+// Workspace: headers first, then the partial rows.
+void paged_step_carve(PagedArgs& a, void* workspace) {
+  a.head = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(a.head + 4 * kGridMax);
+}
+
+cudaError_t launch_paged_step(const PagedArgs& args, const PagedShape& s,
+                              void* workspace, cudaStream_t stream) {
+  PagedArgs a = args;
+  paged_step_carve(a, workspace);
+  return s.head_dim == 128 ? launch_d<128>(a, s, stream)
+                           : launch_d<64>(a, s, stream);
+}
+
+}  // namespace tilemix

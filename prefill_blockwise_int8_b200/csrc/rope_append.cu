@@ -1,0 +1,285 @@
+// Rotary positions of Q and K, and the append of new K / V rows to the pages
+// of the cache (rotated on the way, 16-bit or INT8).
+//
+// Mathematics.  Pair i of a token at position p turns by a = p f_i: (x_a,
+// x_b) -> (x_a c - x_b s, x_b c + x_a s).  The angle is formed in double, p
+// f_i / 2 pi is reduced to [-1/2, 1/2] turns there, and only the remainder
+// becomes fp32, so the rotation of position 10^6 is as exact as that of 10.
+// INT8 rows take absmax / 127 over their d channels (of the row as rounded to
+// 16 bits, so that append(x) after a rotary call and the fused append agree
+// bit for bit) and the quantiser's code definition (quant_code.cuh).
+//
+// What bounds it: memory traffic.  One block takes a few tokens: its threads
+// first make the tokens' cosines and sines (shared by all heads) in shared
+// memory, then every thread walks units of two 16-byte vectors, which hold
+// eight whole pairs in either layout, over the heads of its token.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "paged.h"
+#include "quant_code.cuh"
+
+namespace tilemix {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr double kInvTwoPi = 0.15915494309189533577;
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      half2_bits_to_float2(w[i], f[2 * i], f[2 * i + 1]);
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rotates the eight pairs of a unit.  HALF: a holds the pairs' first
+// channels, b their second ones; INTERLEAVED: a is pairs 0..3, b pairs 4..7.
+// One product rounds before the fused multiply-add, as written.
+__device__ __forceinline__ void turn1(float& x, float& y, float2 t) {
+  const float nx = __fmaf_rn(x, t.x, -__fmul_rn(y, t.y));
+  const float ny = __fmaf_rn(y, t.x, __fmul_rn(x, t.y));
+  x = nx;
+  y = ny;
+}
+
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8],
+                                     const float2* cs, bool interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn1(a[2 * i], a[2 * i + 1], cs[i]);
+      turn1(b[2 * i], b[2 * i + 1], cs[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn1(a[i], b[i], cs[i]);
+  }
+}
+
+// The last sequence whose start is <= t (a warp looks at 32 starts a step);
+// always in [0, batch).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch,
+                                             int t, int lane) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const unsigned below =
+        __ballot_sync(0xffffffffu, i < hi && cu[i] <= t);
+    // starts do not decrease in a valid call, so the set bits are the low
+    // ones; a decreasing cu_seqlens only changes which sequence is checked
+    const int n = max(__popc(below) - 1, 0);
+    lo = lo + n * step;
+    hi = min(lo + step, hi);
+  }
+  return lo;
+}
+
+// Where a token's rows go (append): page id and slot, or page < 0.
+struct Place {
+  int page, slot, pos;
+};
+
+template <bool BF16, int MODE>  // 0 rotary, 1 append 16-bit, 2 append INT8
+__global__ void __launch_bounds__(kThreads)
+    rope_kernel(const __grid_constant__ RopeArgs p, int tokens_per_block) {
+  extern __shared__ float2 cs_all[];  // [tokens_per_block][rot_dim / 2]
+  __shared__ Place place[kThreads / 32];
+  const int t0 = blockIdx.x * tokens_per_block;
+  const int nt = min(tokens_per_block, p.total_tokens - t0);
+  const int half = p.rot_dim >> 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (MODE != 0) {
+    // one warp per token finds its sequence and checks its place
+    if (warp < nt) {
+      const int t = t0 + warp;
+      Place pl{-1, 0, 0};
+      if (t < p.cu_seqlens[p.batch]) {
+        const int b = find_sequence(p.cu_seqlens, p.batch, t, lane);
+        const int start = p.cu_seqlens[b], end = p.cu_seqlens[b + 1];
+        const int len = p.kv_lens[b];
+        const long long pos = static_cast<long long>(len) - (end - start) + (t - start);
+        if (start < 0 || t < start || t >= end || end > p.total_tokens ||
+            len < end - start ||
+            len > (static_cast<long long>(p.max_pages) << p.page_shift)) {
+          if (lane == 0) report_status(p.status, kStatusBadSeqlens);
+        } else {
+          const int page =
+              p.page_table[b * p.table_stride + (pos >> p.page_shift)];
+          if (page < 0 || page >= p.num_pages) {
+            if (lane == 0) report_status(p.status, kStatusBadPages);
+          } else {
+            pl = Place{page, static_cast<int>(pos & ((1 << p.page_shift) - 1)),
+                       static_cast<int>(pos)};
+          }
+        }
+      }
+      if (lane == 0) place[warp] = pl;
+    }
+    __syncthreads();
+  }
+  if (p.freqs) {
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+      const int tt = i / half, j = i - tt * half;
+      int pos;
+      if (MODE != 0) {
+        if (place[tt].page < 0) continue;
+        pos = p.positions ? p.positions[t0 + tt] : place[tt].pos;
+      } else {
+        pos = p.positions[t0 + tt];
+      }
+      const double turns = static_cast<double>(pos) * p.freqs[j] * kInvTwoPi;
+      const float r = static_cast<float>(turns - rint(turns));
+      float s, c;
+      sincospif(2.0f * r, &s, &c);
+      cs_all[i] = make_float2(c * p.attn_factor, s * p.attn_factor * p.sign);
+    }
+  }
+  __syncthreads();
+
+  // Units of a head: rot_dim / 16 rotated ones, then pass-through pairs of
+  // vectors.  A head's units sit on neighbouring threads.
+  const int units = p.head_dim >> 4;
+  const int rot_units = p.freqs ? p.rot_dim >> 4 : 0;
+  const int slots = kThreads / units;  // heads in flight
+  const int u = threadIdx.x % units;
+  const int slot0 = threadIdx.x / units;
+  const int heads = p.hq + p.hk + p.hv;
+  const bool rotated = u < rot_units;
+  // first and second vector of the unit (in vectors of 8 channels)
+  int v0, v1;
+  if (rotated && !p.interleaved) {
+    v0 = u;
+    v1 = u + rot_units;
+  } else {
+    v0 = 2 * u;
+    v1 = 2 * u + 1;
+  }
+  for (int tt = 0; tt < nt; ++tt) {
+    if (MODE != 0 && place[tt].page < 0) continue;
+    const int64_t t = t0 + tt;
+    const float2* cs = cs_all + tt * half + 8 * u;
+    // Every lane runs the same number of rounds: INT8 rows reduce over lanes.
+    for (int h0 = 0; h0 < heads; h0 += slots) {
+      const int h = h0 + slot0;
+      const bool live = slot0 < slots && h < heads;
+      const bool is_q = h < p.hq, is_v = h >= p.hq + p.hk;
+      const int hl = is_q ? h : is_v ? h - p.hq - p.hk : h - p.hq;
+      const RowTensor in = is_q ? p.q : is_v ? p.v : p.k;
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (live) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(in.p + t * in.st + hl * in.sh);
+        a = src[v0];
+        b = src[v1];
+      }
+      if (rotated && !is_v) {
+        float fa[8], fb[8];
+        unpack8<BF16>(a, fa);
+        unpack8<BF16>(b, fb);
+        turn(fa, fb, cs, p.interleaved != 0);
+        a = pack8<BF16>(fa);
+        b = pack8<BF16>(fb);
+      }
+      if (MODE == 0 || is_q) {
+        if (live) {
+          const RowTensor out = is_q ? p.q_out : p.k_out;
+          uint4* dst = reinterpret_cast<uint4*>(out.p + t * out.st + hl * out.sh);
+          dst[v0] = a;
+          dst[v1] = b;
+        }
+        if (MODE != 2) continue;
+      }
+      const int64_t at = place[tt].page * p.page_stride +
+                         place[tt].slot * p.token_stride + hl * p.head_stride;
+      if (MODE == 1) {
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(
+              static_cast<uint16_t*>(is_v ? p.v_pages : p.k_pages) + at);
+          dst[v0] = a;
+          dst[v1] = b;
+        }
+      } else if (MODE == 2) {
+        float fa[8], fb[8];
+        unpack8<BF16>(a, fa);
+        unpack8<BF16>(b, fb);
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          m = fmaxf(m, fmaxf(fabsf(fa[i]), fabsf(fb[i])));
+        // units is 4 or 8 (head_dim 64 or 128): a head's lanes are an
+        // aligned group of that many
+        for (int o = units >> 1; o > 0; o >>= 1)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (live && !is_q) {
+          const float s = __fdiv_rn(m, 127.0f);
+          const float rcp = m != 0.0f ? __frcp_rn(s) : 0.0f;
+          uint32_t ca[8], cb[8];
+          quant_codes8(fa, s, rcp, ca);
+          quant_codes8(fb, s, rcp, cb);
+          int8_t* row = static_cast<int8_t*>(is_v ? p.v_pages : p.k_pages) + at;
+          *reinterpret_cast<uint2*>(row + v0 * 8) =
+              make_uint2(pack_low_bytes4(ca[0], ca[1], ca[2], ca[3]),
+                         pack_low_bytes4(ca[4], ca[5], ca[6], ca[7]));
+          *reinterpret_cast<uint2*>(row + v1 * 8) =
+              make_uint2(pack_low_bytes4(cb[0], cb[1], cb[2], cb[3]),
+                         pack_low_bytes4(cb[4], cb[5], cb[6], cb[7]));
+          if (u == 0) {
+            const int hkv = p.hk;
+            (is_v ? p.v_scale : p.k_scale)
+                [((static_cast<int64_t>(place[tt].page) * hkv + hl)
+                  << p.page_shift) +
+                 place[tt].slot] = s;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <bool BF16, int MODE>
+cudaError_t launch_one(const RopeArgs& a, cudaStream_t stream) {
+  const int tpb = a.total_tokens >= 1024 ? 4 : 1;
+  const int grid = (a.total_tokens + tpb - 1) / tpb;
+  const size_t smem = a.freqs ? tpb * (a.rot_dim / 2) * sizeof(float2) : 0;
+  rope_kernel<BF16, MODE><<<grid, kThreads, smem, stream>>>(a, tpb);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, bool bf16, int mode,
+                        cudaStream_t stream) {
+  if (mode == 0)
+    return bf16 ? launch_one<true, 0>(a, stream) : launch_one<false, 0>(a, stream);
+  if (mode == 1)
+    return bf16 ? launch_one<true, 1>(a, stream) : launch_one<false, 1>(a, stream);
+  return bf16 ? launch_one<true, 2>(a, stream) : launch_one<false, 2>(a, stream);
+}
+
+}  // namespace tilemix

@@ -10,27 +10,28 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <string>
 
+#include "api_common.h"
 #include "internal.h"
 #include "tilemix.h"
 
+namespace tilemix {
 namespace {
-
-thread_local std::string g_last_error;
+thread_local char g_last_error[512];  // fixed: reporting an error never throws
+}  // namespace
 
 tilemix_status fail(tilemix_status st, const char* fmt, ...) {
-  char buf[512];
+  char buf[sizeof(g_last_error)];  // an argument may be the last error itself
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
+  memcpy(g_last_error, buf, sizeof(buf));
   return st;
 }
 
 tilemix_status ok() {
-  g_last_error.clear();
+  g_last_error[0] = 0;
   return TILEMIX_OK;
 }
 
@@ -65,6 +66,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+}  // namespace tilemix
+
+namespace {
+
+using tilemix::aligned;
+using tilemix::check_device;
+using tilemix::encode_fn;
+using tilemix::fail;
+using tilemix::ok;
 
 // 3-D map over a token-major [T, H, d] tensor: dims {d, T, H}; a box of
 // {box_x elements, box_rows tokens, 1 head}.
@@ -102,13 +113,14 @@ const char* tilemix_status_string(tilemix_status s) {
     case TILEMIX_ERR_TIMEOUT: return "device pipeline wait timed out";
     case TILEMIX_ERR_BAD_SEQLENS: return "invalid cu_seqlens or head_map";
     case TILEMIX_ERR_NO_DEVICE: return "no sm_100 device";
+    case TILEMIX_ERR_BAD_PAGES: return "invalid page table entry";
   }
   return "unknown status";
 }
 
-const char* tilemix_last_error(void) { return g_last_error.c_str(); }
+const char* tilemix_last_error(void) { return tilemix::g_last_error; }
 
-uint32_t tilemix_version(void) { return (1u << 16) | 0u; }
+uint32_t tilemix_version(void) { return (1u << 16) | 1u; }
 
 tilemix_status tilemix_quantize_blockwise(const void* x,
                                           const int32_t* cu_seqlens, int batch,
