@@ -4,6 +4,7 @@
 // INT8 -> fp16 conversion of the INT8 KV cache.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -70,6 +71,25 @@ __device__ __forceinline__ void i8x4_to_h2x2(uint32_t w, uint32_t& lo,
   __half2 hb = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
   lo = *reinterpret_cast<uint32_t*>(&ha);
   hi = *reinterpret_cast<uint32_t*>(&hb);
+}
+
+// Four int8 codes -> two bf16 pairs, exactly: |low 7 bits| under the bf16
+// exponent of 128 minus 128 or, for a set sign bit, minus 256.
+__device__ __forceinline__ void i8x4_to_bf2x2(uint32_t w, uint32_t& lo,
+                                              uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0u, 0x4140), b = __byte_perm(w, 0u, 0x4342);
+  const uint32_t am = (a & 0x007f007fu) | 0x43004300u;
+  const uint32_t as = (a & 0x00800080u) | 0x43004300u;
+  const uint32_t bm = (b & 0x007f007fu) | 0x43004300u;
+  const uint32_t bs = (b & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 x =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&am),
+              *reinterpret_cast<const __nv_bfloat162*>(&as));
+  const __nv_bfloat162 y =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&bm),
+              *reinterpret_cast<const __nv_bfloat162*>(&bs));
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 // One key row of an INT8 tile (D bytes at row rr of `src`, swizzled with

@@ -1,0 +1,738 @@
+// Attention of many new tokens over a paged KV cache (a prompt's chunk,
+// verified drafts, a decoder over an encoder's states).
+//
+// Mathematics.  As in the step kernel: the query heads of one KV head and
+// the new tokens pack into rows; per row a running maximum m (base-2 logits,
+// moved lazily: only when a key exceeds it by more than 2^8), sum l and
+// unnormalised output O.  INT8 pages: K codes convert exactly to the query's
+// type and their scale multiplies the fp32 score; V codes convert exactly to
+// fp16 and their scale joins P as P sv 2^-E, 2^E a power of two near the
+// scales seen (raised, with O rescaled, when a scale passes 32 times it), so
+// that products stay inside fp16's range.
+//
+// B200 design.  One CTA per SM takes an equal part of the line of all items
+// (256 packed rows of a sequence and KV head, times its keys in units of
+// 128); an item cut between CTAs leaves partial results for the merge
+// kernel.  Inside a CTA:
+//   warps 0-3, 4-7  softmax of the two 128-row query tiles, one thread per
+//               row (= TMEM lane) with the row's 128 scores in registers: no
+//               exchange between threads.  They load Q (any group size and
+//               stride), write P over the scores they have read, rescale O
+//               when a maximum moves, and finish O / l;
+//   warp 8      TMA producer: pages through {64 channels, page} boxes into
+//               one ring of K and V tiles (INT8: raw tiles and scales);
+//   warp 9      issues tcgen05.mma: S_t = Q_t K^T and O_t += P_t V with P_t
+//               in TMEM, in the order PV_0, S_0, PV_1, S_1, so one tile's
+//               softmax runs while the other's products do; clears the rows
+//               of the last V tile behind the sequence's end;
+//   warps 12-15 (INT8) convert raw tiles to 16-bit ones.
+// TMEM: S_0 O_0 S_1 O_1, 128 columns each; P_t over the first 64 of S_t.
+#include <cuda.h>
+
+#include "attn_common.cuh"
+#include "paged_common.cuh"
+
+namespace tilemix {
+namespace {
+
+constexpr int kM = 128;       // rows of a query tile = TMEM lanes
+constexpr int kRows = 2 * kM; // packed rows of an item
+constexpr int kN = 128;       // keys of a unit
+constexpr int kGridMax = 148;
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpConv = 12;
+constexpr int kScRing = 4;    // tiles whose INT8 scales are kept
+constexpr int kBadRing = 8;   // segments whose page check is kept
+
+template <int D, bool INT8>
+struct Cfg {
+  static constexpr int kThreads = INT8 ? 512 : 384;
+  // Registers after the split: softmax warps (256 threads) and the others;
+  // 256 a + (kThreads - 256) b = the launch's total (512 * 128, 384 * 168).
+  static constexpr int kRegsSoftmax = INT8 ? 184 : 208;
+  static constexpr int kRegsOther = INT8 ? 72 : 88;
+  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther ==
+                kThreads * (INT8 ? 128 : 168), "register split");
+  static constexpr int kQTile = kM * D * 2;
+  static constexpr int kTile = kN * D * 2;
+  static constexpr int kSlots = INT8 ? 3 : D == 128 ? 5 : 8;
+  static constexpr int kRaw = kN * D;
+  static constexpr int kRawSlots = INT8 ? 3 : 0;
+  static constexpr int kRingOff = 2 * kQTile;
+  static constexpr int kRawOff = kRingOff + kSlots * kTile;
+  static constexpr int kRawScOff = kRawOff + kRawSlots * kRaw;  // [raw][128]
+  static constexpr int kKscOff = kRawScOff + kRawSlots * kN * 4;
+  static constexpr int kVscOff = kKscOff + (INT8 ? kScRing * kN * 4 : 0);
+  static constexpr int kExpOff = kVscOff + (INT8 ? kScRing * kN * 4 : 0);
+  static constexpr int kBadOff = kExpOff + 4 * kScRing;
+  static constexpr int kBarOff = kBadOff + 4 * kBadRing;
+  // barriers
+  static constexpr int kBarQ = 0;                    // [tile]
+  static constexpr int kBarS = 2;                    // [tile]
+  static constexpr int kBarP = 4;                    // [tile][half]
+  static constexpr int kBarO = 8;                    // [tile]
+  static constexpr int kBarFull = 10;                // [slot]
+  static constexpr int kBarEmpty = kBarFull + kSlots;
+  static constexpr int kBarRawFull = kBarEmpty + kSlots;
+  static constexpr int kBarRawEmpty = kBarRawFull + kRawSlots;
+  static constexpr int kBarKsc = kBarRawEmpty + kRawSlots;  // [kScRing]
+  static constexpr int kBarVsc = kBarKsc + (INT8 ? kScRing : 0);
+  static constexpr int kBarDrain = kBarVsc + (INT8 ? kScRing : 0);
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kSmem = kBarOff + 8 * kNumBars + 16 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kBarOff % 8 == 0, "barrier alignment");
+};
+
+// What the warps of a CTA know of a segment (an item's units [ua, ub)).
+struct Segment {
+  SeqGeom g;
+  int kvh, ua, ub, units;
+  int nrows, tok0, head0;
+  int keys;   // of the item's last row
+  int index;  // segments before it
+};
+
+// Calls f(segment) for this CTA's part of the line, in order, until f
+// returns false.  Every warp walks it by itself.
+template <class F>
+__device__ __forceinline__ void for_segments(const PagedArgs& p,
+                                             const Line<kRows, kN>& line,
+                                             Cursor cur, const Cursor& end,
+                                             F&& f) {
+  int index = 0;
+  while (cur.b < p.batch) {
+    Segment s;
+    s.g = seq_geom(p, cur.b, false);
+    const bool at_end = same_item(cur, end);
+    s.units = line.units(p, s.g, cur.qt);
+    s.ua = cur.unit;
+    s.ub = at_end ? end.unit : s.units;
+    if (s.ua < s.ub) {
+      s.kvh = cur.kvh;
+      s.nrows = line.rows(p, s.g, cur.qt);
+      s.tok0 = line.first_token(cur.qt);
+      s.head0 = cur.kvh * p.group + line.first_head(cur.qt);
+      s.keys = line.keys(p, s.g, cur.qt);
+      s.index = index++;
+      if (!f(s, cur.b)) return;
+    }
+    if (at_end) return;
+    cur = line.next(p, s.g, cur);
+  }
+}
+
+// One key row of codes (D bytes at row r of `src`, swizzled) -> 16-bit row r
+// of a K or V tile (D/64 chunks of [128][128 B], 128-byte swizzle).
+template <int D, bool BF16>
+__device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst,
+                                              int r) {
+  constexpr uint32_t sm = D == 128 ? 7u : 3u;
+#pragma unroll
+  for (int u = 0; u < D / 16; ++u) {
+    const uint4 in = *reinterpret_cast<const uint4*>(src + swz(r * D + u * 16, sm));
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (BF16) i8x4_to_bf2x2(w[i], h[2 * i], h[2 * i + 1]);
+      else i8x4_to_h2x2(w[i], h[2 * i], h[2 * i + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t o = (u >> 2) * (kN * 128) + r * 128 + ((2 * u + e) & 7) * 16;
+      *reinterpret_cast<uint4*>(dst + swz(o, 7)) =
+          make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+    }
+  }
+}
+
+template <int D, bool BF16, bool INT8>
+__global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
+    chunk_kernel(const __grid_constant__ PagedArgs p) {
+  using C = Cfg<D, INT8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  clear_headers(p);
+  const Line<kRows, kN> line(p);
+  const long long total = line.total(p, lane, blockIdx.x == 0 && warp == 0);
+  const long long w0 = total * blockIdx.x / gridDim.x;
+  const long long w1 = total * (blockIdx.x + 1) / gridDim.x;
+  pdl_launch();
+  if (w0 >= w1) return;
+  const Cursor begin = line.locate(p, w0, lane);
+  const Cursor end = line.locate(p, w1, lane);
+
+  uint8_t* ring = smem + C::kRingOff;
+  float* ksc = reinterpret_cast<float*>(smem + C::kKscOff);
+  float* vsc = reinterpret_cast<float*>(smem + C::kVscOff);
+  volatile float* vexp = reinterpret_cast<volatile float*>(smem + C::kExpOff);
+  volatile int* bad_ring = reinterpret_cast<volatile int*>(smem + C::kBadOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  if (warp == kWarpProducer && lane == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars[C::kBarQ + t], 4);  // one arrival per softmax warp
+      mbar_init(&bars[C::kBarS + t], 1);
+      mbar_init(&bars[C::kBarP + 2 * t], 4);
+      mbar_init(&bars[C::kBarP + 2 * t + 1], 4);
+      mbar_init(&bars[C::kBarO + t], 1);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&bars[C::kBarFull + s], INT8 ? 4 : 1);
+      mbar_init(&bars[C::kBarEmpty + s], 1);
+    }
+    if (INT8) {
+      for (int s = 0; s < C::kRawSlots; ++s) {
+        mbar_init(&bars[C::kBarRawFull + s], 1);
+        mbar_init(&bars[C::kBarRawEmpty + s], 4);
+      }
+      for (int s = 0; s < kScRing; ++s) {
+        mbar_init(&bars[C::kBarKsc + s], 4);
+        mbar_init(&bars[C::kBarVsc + s], 4);
+      }
+    }
+    mbar_init(&bars[C::kBarDrain], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    report_status(p.status, kStatusTimeout);
+  };
+  // warp-wide wait; false once some wait ran out anywhere in the CTA
+  auto wait = [&](int bar, uint32_t parity) -> bool {
+    const bool got = mbar_wait(&bars[bar], parity & 1u, abort_flag);
+    return __all_sync(0xffffffffu, got);
+  };
+
+  if (warp >= 8) {
+    regs_dec<C::kRegsOther>();
+    if (warp == kWarpProducer) {
+      // =================== TMA producer ===================
+      // A tile's K and V come in pieces of min(page, 128) keys; lane l
+      // issues piece l / chunks, channel chunk l % chunks.
+      constexpr int kChunks = INT8 ? 1 : D / 64;
+      constexpr int kStages = INT8 ? C::kRawSlots : C::kSlots;
+      constexpr int kFull = INT8 ? C::kBarRawFull : C::kBarFull;
+      constexpr int kEmpty = INT8 ? C::kBarRawEmpty : C::kBarEmpty;
+      const int bt_shift = min(p.page_shift, 7);
+      const int bt = 1 << bt_shift;  // keys of a piece
+      const int piece = lane / kChunks, chunk = lane % kChunks;
+      uint32_t idx = 0;  // tiles loaded
+      bool ok = true;
+      for_segments(p, line, begin, end, [&](const Segment& s, int b) {
+        if (lane == 0) bad_ring[s.index % kBadRing] = 0;
+        __syncwarp();
+        const int32_t* trow = p.page_table + b * p.table_stride;
+        auto loads = [&](int n) {  // this lane has a piece of tile n
+          return piece * bt < kN && n * kN + piece * bt < s.g.len;
+        };
+        auto page_of = [&](int n) {
+          return loads(n) ? trow[(n * kN + piece * bt) >> p.page_shift] : 0;
+        };
+        int id_next = page_of(s.ua);
+        for (int n = s.ua; n < s.ub && ok; ++n) {
+          int id = id_next;
+          if (n + 1 < s.ub) id_next = page_of(n + 1);
+          const bool load = loads(n);
+          if (load && (id < 0 || id >= p.num_pages)) {
+            report_status(p.status, kStatusBadPages);
+            bad_ring[s.index % kBadRing] = 1;
+            id = 0;
+          }
+          const int live = min(kN, s.g.len - n * kN);
+          const uint32_t pieces = live > 0 ? (live + bt - 1) >> bt_shift : 0;
+          const uint32_t bytes =
+              pieces * bt * (INT8 ? D + 4 : D * 2);
+          const int slot_key = (n * kN + piece * bt) & ((1 << p.page_shift) - 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t st = idx % kStages;
+            if (idx >= kStages && !wait(kEmpty + st, idx / kStages - 1)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&bars[kFull + st], bytes);
+            __syncwarp();
+            if (load) {
+              const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
+              uint64_t* bar = &bars[kFull + st];
+              if (INT8) {
+                tma_load_4d(smem + C::kRawOff + st * C::kRaw + piece * bt * D, tm,
+                            bar, 0, slot_key, s.kvh, id);
+                const float* sc = kv ? p.v_scale : p.k_scale;
+                bulk_load(smem + C::kRawScOff + (st * kN + piece * bt) * 4,
+                          sc + (((static_cast<int64_t>(id) * p.hkv + s.kvh)
+                                 << p.page_shift) + slot_key),
+                          bt * 4, bar);
+              } else {
+                tma_load_4d(ring + st * C::kTile + chunk * (kN * 128) +
+                                piece * bt * 128,
+                            tm, bar, chunk * 64, slot_key, s.kvh, id);
+              }
+            }
+            ++idx;
+          }
+        }
+        return ok;
+      });
+      if (!ok) fail();
+      // copies in flight land (bounded) before the CTA may exit
+      const uint32_t first = idx > kStages ? idx - kStages : 0;
+      if (!ok)
+        for (uint32_t i = first; i < idx; ++i)
+          mbar_wait(&bars[kFull + i % kStages], (i / kStages) & 1, nullptr);
+    } else if (warp == kWarpMma) {
+      // =================== MMA issuer ===================
+      constexpr uint32_t kFmtQ = BF16 ? 1 : 0;
+      constexpr uint32_t kFmtP = BF16 && !INT8 ? 1 : 0;
+      constexpr uint32_t id_s = instr_desc(1, kFmtQ, kFmtQ, 0, 0, kN, kM);
+      constexpr uint32_t id_o = instr_desc(1, kFmtP, kFmtP, 0, 1, D, kM);
+      const uint64_t dq = desc_k_f16(smem_u32(smem), kM * 128, 0);
+      const uint64_t dk = desc_k_f16(smem_u32(ring), kN * 128, 0);
+      const uint64_t dv = desc_v(smem_u32(ring), kN * 128, 0);
+      uint32_t idx = 0;                 // tiles consumed (K and V count each)
+      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};
+      bool ok = true;
+      auto issue_s = [&](int t, uint32_t slot) {
+        if (lane == 0) {
+          const uint64_t q = dq + t * (C::kQTile >> 4);
+          const uint64_t k = dk + static_cast<uint64_t>(slot) * (C::kTile >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t o = (ks >> 2) * (kM * 128 / 16) + k_step(ks);
+            mma_f16_ss(tmem + t * 256, q + o, k + o, id_s, ks > 0 ? 1u : 0u);
+          }
+          mma_commit(&bars[C::kBarS + t]);
+        }
+        __syncwarp();
+      };
+      for_segments(p, line, begin, end, [&](const Segment& s, int) {
+        const int tiles = s.nrows > kM ? 2 : 1;
+        auto full = [&](uint32_t i) {
+          return ok = wait(C::kBarFull + i % C::kSlots, i / C::kSlots);
+        };
+        auto free_slot = [&](uint32_t i) {
+          if (lane == 0) mma_commit(&bars[C::kBarEmpty + i % C::kSlots]);
+          __syncwarp();
+        };
+        if (!full(idx)) return false;
+        for (int t = 0; t < tiles; ++t) {
+          if (!(ok = wait(C::kBarQ + t, nq[t]++))) return false;
+          tc_fence_after();
+          issue_s(t, idx % C::kSlots);
+        }
+        free_slot(idx);
+        for (int n = s.ua; n < s.ub; ++n) {
+          const uint32_t iv = idx + 1, ik = idx + 2;
+          const bool last = n + 1 == s.ub;
+          const uint32_t vslot = iv % C::kSlots;
+          for (int t = 0; t < tiles; ++t) {
+            if (t == 0) {
+              if (!full(iv)) return false;
+              const int live = s.g.len - n * kN;
+              if (!INT8 && live < kN) {
+                // rows behind the sequence's end may hold anything: P there
+                // is 0, but 0 times NaN is not
+                const int r0 = max(live, 0);
+                for (int c = 0; c < D / 64; ++c) {
+                  uint4* z = reinterpret_cast<uint4*>(ring + vslot * C::kTile +
+                                                      c * (kN * 128) + r0 * 128);
+                  for (int i = lane; i < (kN - r0) * 8; i += 32)
+                    z[i] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
+            const uint32_t tb = tmem + t * 256;
+            const uint64_t v = dv + static_cast<uint64_t>(vslot) * (C::kTile >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!(ok = wait(C::kBarP + 2 * t + h, np[t]))) return false;
+              tc_fence_after();
+              if (lane == 0) {
+#pragma unroll
+                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                  mma_f16_ts(tb + 128, tb + ks * 8, v + ks * (16 * 128 / 16), id_o,
+                             n > s.ua || ks > 0 ? 1u : 0u);
+              }
+              __syncwarp();
+            }
+            ++np[t];
+            if (last) {
+              if (lane == 0) mma_commit(&bars[C::kBarO + t]);
+              __syncwarp();
+            } else {
+              if (t == 0) {
+                if (!full(ik)) return false;
+                tc_fence_after();
+              }
+              issue_s(t, ik % C::kSlots);
+            }
+          }
+          free_slot(iv);
+          if (!last) free_slot(ik);
+          idx += 2;
+        }
+        return true;
+      });
+      if (!ok) fail();
+      // every MMA issued above has finished once this completes
+      if (lane == 0) {
+        mma_commit(&bars[C::kBarDrain]);
+        mbar_wait(&bars[C::kBarDrain], 0, nullptr);
+      }
+      __syncwarp();
+    } else if (INT8 && warp >= kWarpConv) {
+      // =================== INT8 converters (4 warps) ===================
+      const int r = (warp - kWarpConv) * 32 + lane;  // key row of a tile
+      uint32_t idx = 0, tile = 0;
+      float inv = 0.0f;  // 2^-E; 0 while no scale has been seen
+      bool ok = true;
+      for_segments(p, line, begin, end, [&](const Segment& s, int) {
+        inv = 0.0f;  // O begins anew with every segment
+        for (int n = s.ua; n < s.ub; ++n, ++tile) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++idx) {
+            const uint32_t raw = idx % (INT8 ? C::kRawSlots : 1);
+            const uint32_t st = idx % C::kSlots;
+            const uint32_t sr = tile % kScRing;
+            if (!wait(C::kBarRawFull + raw, idx / (INT8 ? C::kRawSlots : 1)) ||
+                (idx >= C::kSlots && !wait(C::kBarEmpty + st, idx / C::kSlots - 1))) {
+              ok = false;
+              return false;
+            }
+            const float* sc =
+                reinterpret_cast<const float*>(smem + C::kRawScOff) + raw * kN;
+            const int live = s.g.len - n * kN;
+            uint8_t* dst = ring + st * C::kTile;
+            const uint8_t* src = smem + C::kRawOff + raw * C::kRaw;
+            if (kv == 0) {
+              ksc[sr * kN + r] = r < live ? sc[r] * p.scale_log2 : 0.0f;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[C::kBarKsc + sr]);
+              convert_codes<D, BF16>(src, dst, r);
+            } else {
+              float top = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (4 * lane + j < live) top = fmaxf(top, fabsf(sc[4 * lane + j]));
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              if (top > 0.0f && (inv == 0.0f || top * inv > 32.0f)) {
+                const int e = min(max(ilogbf(top) + 1, -126), 126);
+                inv = ldexpf(1.0f, -e);
+              }
+              vsc[sr * kN + r] = r < live ? sc[r] * inv : 0.0f;
+              if (r == 0) vexp[sr] = inv;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[C::kBarVsc + sr]);
+              // rows behind the end: any code is finite, and P is 0 there
+              convert_codes<D, false>(src, dst, r);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bars[C::kBarFull + st]);
+              mbar_arrive(&bars[C::kBarRawEmpty + raw]);
+            }
+          }
+        }
+        return true;
+      });
+      if (!ok) fail();
+    }
+  } else {
+    regs_inc<C::kRegsSoftmax>();
+    // =================== softmax ===================
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;  // row of the tile
+    const uint32_t ta =
+        tmem + t * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    uint8_t* sq = smem + t * C::kQTile;
+    uint32_t ns = 0, no = 0;  // S tiles and segments seen
+    uint32_t tile = 0;        // tiles of all segments
+    bool ok = true;
+    for_segments(p, line, begin, end, [&](const Segment& s, int) {
+      if (t * kM >= s.nrows) {
+        tile += s.ub - s.ua;
+        return true;
+      }
+      // ---- Q: D/8 threads a row, 16 bytes each ----
+      {
+        constexpr int kU = D / 8, kStep = kM / kU;
+        const int u = r % kU;
+        uint4 x[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int row = t * kM + r / kU + k * kStep;
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (row < s.nrows)
+            x[k] = *reinterpret_cast<const uint4*>(
+                p.q + static_cast<int64_t>(s.g.start + s.tok0 + row / p.group) * p.q_st +
+                static_cast<int64_t>(s.head0 + row % p.group) * p.q_sh + u * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int row = r / kU + k * kStep;
+          *reinterpret_cast<uint4*>(
+              sq + swz((u >> 3) * (kM * 128) + row * 128 + (u & 7) * 16, 7)) = x[k];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::kBarQ + t]);
+      }
+      const int row = t * kM + r;
+      const int lim = row < s.nrows
+                          ? keys_of_token(p, s.g, s.tok0 + row / p.group)
+                          : 0;
+      // keys that every live row of the warp's tile sees
+      const int lim_min = keys_of_token(p, s.g, s.tok0 + t * kM / p.group);
+      float m_run = -CUDART_INF_F, l_run = 0.0f;
+      float inv = 0.0f;
+      for (int n = s.ua; n < s.ub; ++n, ++tile) {
+        const uint32_t sr = tile % kScRing;
+        if (!wait(C::kBarS + t, ns)) return ok = false;
+        ++ns;
+        tc_fence_after();
+        uint32_t sv[kN];
+        tmem_ld32_at(ta, sv, 0);
+        tmem_ld32_at(ta, sv, 32);
+        tmem_ld32_at(ta, sv, 64);
+        tmem_ld32_at(ta, sv, 96);
+        if (INT8 && !wait(C::kBarKsc + sr, tile / kScRing)) return ok = false;
+        tmem_ld_wait();
+        if (INT8) {  // logits: the keys' scales differ
+          const float4* kc = reinterpret_cast<const float4*>(ksc + sr * kN);
+#pragma unroll
+          for (int j = 0; j < kN; j += 4) {
+            const float4 c = kc[j / 4];
+            const float2 a = __fmul2_rn(make_float2(__uint_as_float(sv[j]),
+                                                    __uint_as_float(sv[j + 1])),
+                                        make_float2(c.x, c.y));
+            const float2 b = __fmul2_rn(make_float2(__uint_as_float(sv[j + 2]),
+                                                    __uint_as_float(sv[j + 3])),
+                                        make_float2(c.z, c.w));
+            sv[j] = __float_as_uint(a.x), sv[j + 1] = __float_as_uint(a.y);
+            sv[j + 2] = __float_as_uint(b.x), sv[j + 3] = __float_as_uint(b.y);
+          }
+        }
+        if ((n + 1) * kN > lim_min) {  // by position, whatever the slot held
+          const int hl = lim - n * kN;
+#pragma unroll
+          for (int j = 0; j < kN; ++j)
+            if (j >= hl) sv[j] = 0xff800000u;  // -inf
+        }
+        float mx;
+        {
+          float a[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            a[k] = fmaxf(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
+#pragma unroll
+          for (int j = 16; j < kN; j += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              a[k] = fmax3(a[k], __uint_as_float(sv[j + 2 * k]),
+                           __uint_as_float(sv[j + 2 * k + 1]));
+          mx = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]),
+                     fmaxf(a[6], a[7]));
+        }
+        const float c = INT8 ? 1.0f : p.scale_log2;
+        mx = mx == -CUDART_INF_F ? mx : mx * c;
+        bool need = mx > m_run + kRescaleThreshold;
+        float alpha = 1.0f;
+        if (need) {
+          alpha = ex2_approx(m_run - mx);
+          m_run = mx;
+          l_run *= alpha;
+        }
+        float ve = 0.0f;
+        if (INT8) {
+          if (!wait(C::kBarVsc + sr, tile / kScRing)) return ok = false;
+          ve = vexp[sr];
+          if (ve != inv) {
+            alpha *= inv == 0.0f ? 0.0f : ve / inv;
+            inv = ve;
+            need = true;
+          }
+        }
+        // S_t(n) is ready, so the products before it are done: O_t may be
+        // rescaled now
+        if (n > s.ua && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+          for (int oc = 0; oc < D; oc += 16) {
+            uint32_t o[16];
+            tmem_ld16(ta + 128 + oc, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st16(ta + 128 + oc, o);
+          }
+        }
+        const float mu = m_run == -CUDART_INF_F ? 0.0f : m_run;
+        const float2 c2 = make_float2(c, c), nm = make_float2(-mu, -mu);
+        float2 ps[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ps[k] = make_float2(0.f, 0.f);
+        const float4* vc = reinterpret_cast<const float4*>(vsc + sr * kN);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = 32 * q + 2 * i;
+            const float2 sc =
+                make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
+            const float2 x = INT8 ? __fadd2_rn(sc, nm) : __ffma2_rn(sc, c2, nm);
+            float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            ps[i & 3] = __fadd2_rn(ps[i & 3], e);
+            if (INT8) {
+              const float4 v4 = vc[j / 4];
+              e = __fmul2_rn(e, (i & 1) ? make_float2(v4.z, v4.w)
+                                        : make_float2(v4.x, v4.y));
+            }
+            pk[i] = pack_pair<BF16 && !INT8>(e.x, e.y);
+          }
+          tmem_st16(ta + 16 * q, pk);
+          if (q & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[C::kBarP + 2 * t + (q >> 1)]);
+          }
+        }
+        const float2 s2 =
+            __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
+        l_run += s2.x + s2.y;
+      }
+      // ---- O_t / l, or a partial result ----
+      if (!wait(C::kBarO + t, no)) return ok = false;
+      ++no;
+      tc_fence_after();
+      const bool whole = s.ua == 0 && s.ub == s.units;
+      const bool bad = bad_ring[s.index % kBadRing] != 0;
+      const int slot = 2 * blockIdx.x + (s.ua == 0 ? 1 : 0);
+      const bool live = row < s.nrows && !(whole && bad);
+      const int tok = s.g.start + s.tok0 + row / p.group;
+      const int h = s.head0 + row % p.group;
+      float f = INT8 ? (inv > 0.0f ? 1.0f / inv : 0.0f) : 1.0f;
+      if (whole) f = l_run == 0.0f ? 0.0f : f / l_run;
+      const bool none = whole && l_run == 0.0f;
+      uint16_t* dst = p.out + (static_cast<int64_t>(tok) * p.hq + h) * D;
+      float* prow = part_row<D, kRows>(p, slot, row);
+#pragma unroll 1
+      for (int oc = 0; oc < D; oc += 32) {
+        uint32_t o[32];
+        tmem_ld32(ta + 128 + oc, o);
+        tmem_ld_wait();
+        if (live) {
+          if (whole) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = none ? 0u
+                            : pack_pair<BF16>(__uint_as_float(o[8 * v + 2 * i]) * f,
+                                              __uint_as_float(o[8 * v + 2 * i + 1]) * f);
+              reinterpret_cast<uint4*>(dst + oc)[v] =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              reinterpret_cast<float4*>(prow + oc)[v] = make_float4(
+                  __uint_as_float(o[4 * v]) * f, __uint_as_float(o[4 * v + 1]) * f,
+                  __uint_as_float(o[4 * v + 2]) * f,
+                  __uint_as_float(o[4 * v + 3]) * f);
+          }
+        }
+      }
+      if (live) {
+        if (!whole) {
+          prow[D] = m_run;
+          prow[D + 1] = l_run;
+        } else if (p.lse) {
+          p.lse[static_cast<int64_t>(h) * p.total_tokens + tok] =
+              lse_of(m_run, l_run);
+        }
+      }
+      if (!whole && threadIdx.x == 0) {
+        p.head[2 * slot] =
+            make_int4(1, s.ub == s.units ? 1 : 0, bad ? 1 : 0, s.nrows);
+        p.head[2 * slot + 1] =
+            make_int4(s.g.start + s.tok0, s.head0, p.group, 0);
+      }
+      tc_fence_before();  // these reads come before the next segment's MMAs
+      return true;
+    });
+    if (!ok) fail();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool BF16, bool INT8>
+cudaError_t launch_one(const PagedArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, INT8>;
+  auto kern = chunk_kernel<D, BF16, INT8>;
+  cudaError_t e = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<kGridMax, C::kThreads, C::kSmem, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int rows = static_cast<int>(
+      min(static_cast<long long>(kRows),
+          static_cast<long long>(a.max_q_len) * a.group));
+  return launch_merge<D, BF16, kRows, 1, 8>(a, kGridMax, rows, stream);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs& a, const PagedShape& s,
+                     cudaStream_t stream) {
+  if (s.int8)
+    return s.bf16 ? launch_one<D, true, true>(a, stream)
+                  : launch_one<D, false, true>(a, stream);
+  return s.bf16 ? launch_one<D, true, false>(a, stream)
+                : launch_one<D, false, false>(a, stream);
+}
+
+}  // namespace
+
+size_t paged_chunk_workspace_bytes(int head_dim) {
+  return workspace_of(kGridMax, kRows, head_dim);
+}
+
+cudaError_t launch_paged_chunk(const PagedArgs& args, const PagedShape& s,
+                               void* workspace, cudaStream_t stream) {
+  PagedArgs a = args;
+  carve_workspace(a, workspace, kGridMax);
+  return s.head_dim == 128 ? launch_d<128>(a, s, stream)
+                           : launch_d<64>(a, s, stream);
+}
+
+}  // namespace tilemix

@@ -97,15 +97,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if (BF16) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return pack_half2(lo, hi);
-}
-
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -118,113 +109,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(a));
   return v;
-}
-
-// Four int8 codes -> two bf16 pairs, exactly: |low 7 bits| under the bf16
-// exponent of 128 minus 128 or, for a set sign bit, minus 256.
-__device__ __forceinline__ void i8x4_to_bf2x2(uint32_t w, uint32_t& lo,
-                                              uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0u, 0x4140), b = __byte_perm(w, 0u, 0x4342);
-  const uint32_t am = (a & 0x007f007fu) | 0x43004300u;
-  const uint32_t as = (a & 0x00800080u) | 0x43004300u;
-  const uint32_t bm = (b & 0x007f007fu) | 0x43004300u;
-  const uint32_t bs = (b & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 x =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&am),
-              *reinterpret_cast<const __nv_bfloat162*>(&as));
-  const __nv_bfloat162 y =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&bm),
-              *reinterpret_cast<const __nv_bfloat162*>(&bs));
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
-
-// Position of a unit of work.
-struct Cursor {
-  int b, kvh, qt;
-  int unit;  // unit inside the item
-};
-
-__device__ __forceinline__ int item_units(const PagedArgs& p, const SeqGeom& g,
-                                          int qt) {
-  // keys of the tile's last row
-  const int rows = g.n * p.group;
-  const int last = min((qt + 1) * kRows, rows) - 1;
-  const int keys = keys_of_token(p, g, last / p.group);
-  return max(1, (keys + kUnit - 1) / kUnit);
-}
-
-__device__ __forceinline__ int tiles_of(const PagedArgs& p, const SeqGeom& g) {
-  return (g.n * p.group + kRows - 1) / kRows;
-}
-
-__device__ __forceinline__ long long head_units(const PagedArgs& p,
-                                                const SeqGeom& g) {
-  long long s = 0;
-  const int tiles = tiles_of(p, g);
-  for (int qt = 0; qt < tiles; ++qt) s += item_units(p, g, qt);
-  return s;
-}
-
-// Total units, by all lanes of a warp.
-__device__ __forceinline__ long long total_units(const PagedArgs& p, int lane,
-                                                 bool report) {
-  long long s = 0;
-  for (int b = lane; b < p.batch; b += 32)
-    s += head_units(p, seq_geom(p, b, report)) * p.hkv;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// The item and unit at position w of the line (w < total).
-__device__ __forceinline__ Cursor locate(const PagedArgs& p, long long w,
-                                         int lane) {
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int b = b0 + lane;
-    long long mine = 0, per_head = 0;
-    if (b < p.batch) {
-      per_head = head_units(p, seq_geom(p, b, false));
-      mine = per_head * p.hkv;
-    }
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, incl > w);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      const long long before = __shfl_sync(0xffffffffu, incl - mine, l);
-      const long long ph = __shfl_sync(0xffffffffu, per_head, l);
-      Cursor c;
-      c.b = b0 + l;
-      long long rem = w - before;
-      c.kvh = static_cast<int>(rem / ph);
-      rem -= c.kvh * ph;
-      const SeqGeom g = seq_geom(p, c.b, false);
-      c.qt = 0;
-      while (true) {
-        const int u = item_units(p, g, c.qt);
-        if (rem < u) break;
-        rem -= u;
-        ++c.qt;
-      }
-      c.unit = static_cast<int>(rem);
-      return c;
-    }
-    w -= __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return Cursor{0, 0, 0, 0};  // not reached for w < total
-}
-
-// Partial-result slots: 2 c for an item that began in an earlier block, 2 c
-// + 1 for one that begins in block c and goes on.  Header {used, ends here,
-// bad, rows}; second word of slot 2 c + 1's item: {b, kvh, qt, -}.
-template <int D>
-__device__ __forceinline__ float* part_rows(const PagedArgs& p, int slot) {
-  return p.part + static_cast<size_t>(slot) * kRows * (D + 2);
 }
 
 template <int D, bool BF16, bool INT8>
@@ -250,40 +134,44 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
 
-  const long long total = total_units(p, lane, blockIdx.x == 0 && warp == 0);
+  clear_headers(p);
+  const Line<kRows, kUnit> line(p);
+  const long long total = line.total(p, lane, blockIdx.x == 0 && warp == 0);
   const long long w0 = total * blockIdx.x / gridDim.x;
   const long long w1 = total * (blockIdx.x + 1) / gridDim.x;
-  if (threadIdx.x < 2)
-    p.head[4 * blockIdx.x + 2 * threadIdx.x] = make_int4(0, 0, 0, 0);
+  pdl_launch();
   if (w0 >= w1) return;
-  Cursor cur = locate(p, w0, lane);
-  long long left = w1 - w0;
+  Cursor cur = line.locate(p, w0, lane);
+  const Cursor end = line.locate(p, w1, lane);
   uint32_t issued = 0, consumed = 0;  // ring slots, over all items
   bool dead = false;                  // a wait ran out
 
-  while (left > 0) {
+  while (cur.b < p.batch) {
     const SeqGeom g = seq_geom(p, cur.b, false);
-    const int units = item_units(p, g, cur.qt);
+    const bool at_end = same_item(cur, end);
+    const int units = line.units(p, g, cur.qt);
     const int ua = cur.unit;
-    const int ub = static_cast<int>(min(static_cast<long long>(units), ua + left));
-    const int row0 = cur.qt * kRows;
-    const int nrows = min(kRows, g.n * p.group - row0);
-    const int tok_first = row0 / p.group;
-    const int tok_last = (row0 + nrows - 1) / p.group;
-    const int keys = keys_of_token(p, g, tok_last);     // the tile's limit
-    const int keys_min = keys_of_token(p, g, tok_first);  // its first row's
+    const int ub = at_end ? end.unit : units;
+    if (ua >= ub) {
+      if (at_end) break;
+      cur = line.next(p, g, cur);
+      continue;
+    }
+    const int nrows = line.rows(p, g, cur.qt);
+    const int tok0 = line.first_token(cur.qt);
+    const int head0 = cur.kvh * p.group + line.first_head(cur.qt);
+    const int keys = line.keys(p, g, cur.qt);         // the tile's limit
+    const int keys_min = keys_of_token(p, g, tok0);   // its first row's
     // rows of this thread: g8 and g8 + 8
     int lim[2];
     const uint16_t* qrow[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = g8 + 8 * i;
-      const int pr = row0 + min(r, nrows - 1);
-      const int tok = pr / p.group;
+      const int tok = tok0 + r / p.group;
       lim[i] = r < nrows ? keys_of_token(p, g, tok) : 0;
       qrow[i] = r < nrows ? p.q + static_cast<int64_t>(g.start + tok) * p.q_st +
-                                static_cast<int64_t>(cur.kvh * p.group +
-                                                     pr % p.group) * p.q_sh
+                                static_cast<int64_t>(head0 + r % p.group) * p.q_sh
                           : nullptr;
     }
 
@@ -504,8 +392,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             e4[e] = key0 + key < g.len ? e4[e] * (svv[2 * j + (e & 1)] * inv) : 0.0f;
           }
         }
-        pf[2 * j] = pack2<BF16 && !INT8>(e4[0], e4[1]);
-        pf[2 * j + 1] = pack2<BF16 && !INT8>(e4[2], e4[3]);
+        pf[2 * j] = pack_pair<BF16 && !INT8>(e4[0], e4[1]);
+        pf[2 * j + 1] = pack_pair<BF16 && !INT8>(e4[2], e4[3]);
       }
       // V rows past the sequence's end may hold NaN: cleared in registers
       const bool tail = key0 + kGroup > g.len;
@@ -637,12 +525,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         lt += f[w] * rows[w][D + 1];
       }
       if (r < nrows && !(whole && bad)) {
-        const int pr = row0 + r;
-        const int tok = g.start + pr / p.group;
-        const int h = cur.kvh * p.group + pr % p.group;
-        const float il = lt == 0.0f ? 0.0f : 1.0f / lt;
+        const int tok = g.start + tok0 + r / p.group;
+        const int h = head0 + r % p.group;
+        const float il = 1.0f / lt;
         uint16_t* dst = p.out + (static_cast<int64_t>(tok) * p.hq + h) * D;
-        float* prow = part_rows<D>(p, slot) + r * (D + 2);
+        float* prow = part_row<D, kRows>(p, slot, r);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           const int c = 4 * c8 + 32 * k;
@@ -656,19 +543,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             a.w += f[w] * v.w;
           }
           if (whole) {
-            *reinterpret_cast<uint2*>(dst + c) = make_uint2(
-                pack2<BF16>(a.x * il, a.y * il), pack2<BF16>(a.z * il, a.w * il));
+            *reinterpret_cast<uint2*>(dst + c) =
+                lt == 0.0f ? make_uint2(0u, 0u)
+                           : make_uint2(pack_pair<BF16>(a.x * il, a.y * il),
+                                        pack_pair<BF16>(a.z * il, a.w * il));
           } else {
-            *reinterpret_cast<float2*>(prow + c) = make_float2(a.x, a.y);
-            *reinterpret_cast<float2*>(prow + c + 2) = make_float2(a.z, a.w);
+            *reinterpret_cast<float4*>(prow + c) = a;
           }
         }
         if (c8 == 0) {
           if (whole) {
             if (p.lse)
-              p.lse[static_cast<int64_t>(h) * p.total_tokens + tok] =
-                  lt != 0.0f ? (mt + log2f(lt)) * 0.69314718055994530942f
-                            : -CUDART_INF_F;
+              p.lse[static_cast<int64_t>(h) * p.total_tokens + tok] = lse_of(mt, lt);
           } else {
             prow[D] = mt;
             prow[D + 1] = lt;
@@ -678,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
     if (!whole && threadIdx.x == 0) {
       p.head[2 * slot] = make_int4(1, ub == units ? 1 : 0, bad ? 1 : 0, nrows);
-      p.head[2 * slot + 1] = make_int4(cur.b, cur.kvh, cur.qt, g.start);
+      p.head[2 * slot + 1] = make_int4(g.start + tok0, head0, p.group, 0);
     }
     // the rings take TMA writes again: order the generic accesses before
     fence_proxy_async_smem();
@@ -686,65 +572,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
 
-    left -= ub - ua;
-    cur.unit = 0;
-    if (left > 0) {  // next item (sequences without rows have none)
-      if (++cur.qt >= tiles_of(p, g)) {
-        cur.qt = 0;
-        if (++cur.kvh >= p.hkv) {
-          cur.kvh = 0;
-          do {
-            ++cur.b;
-          } while (cur.b < p.batch - 1 && seq_geom(p, cur.b, false).n == 0);
-        }
-      }
-    }
+    if (at_end) break;
+    cur = line.next(p, g, cur);
   }
-}
-
-// Adds the partial results of the item that begins in block blockIdx.x and
-// goes on in the next ones, row blockIdx.y, in key order.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(D)
-    merge_kernel(const __grid_constant__ PagedArgs p, int blocks) {
-  const int c = blockIdx.x;
-  const int slot = 2 * c + 1;
-  const int4 h = p.head[2 * slot];
-  const int r = blockIdx.y;
-  if (!h.x || r >= h.w) return;
-  const int4 it = p.head[2 * slot + 1];
-  const int ch = threadIdx.x;
-  const float* a = part_rows<D>(p, slot) + r * (D + 2);
-  float m = a[D], l = a[D + 1], o = a[ch];
-  bool bad = h.z != 0, done = false;
-  for (int b = c + 1; b < blocks && !done; ++b) {
-    const int4 n = p.head[4 * b];
-    if (!n.x) continue;  // a block without work
-    bad |= n.z != 0;
-    done = n.y != 0;
-    const float* x = part_rows<D>(p, 2 * b) + r * (D + 2);
-    const float mb = x[D], mn = fmaxf(m, mb);
-    const float mz = mn == -CUDART_INF_F ? 0.0f : mn;
-    const float fa = ex2_approx(m - mz), fb = ex2_approx(mb - mz);
-    o = o * fa + x[ch] * fb;
-    l = l * fa + x[D + 1] * fb;
-    m = mn;
-  }
-  if (bad || !done) return;
-  const int pr = it.z * kRows + r;
-  const int tok = it.w + pr / p.group;
-  const int hq = it.y * p.group + pr % p.group;
-  const float v = l == 0.0f ? 0.0f : o / l;
-  const int64_t at = (static_cast<int64_t>(tok) * p.hq + hq) * D + ch;
-  if (BF16) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    p.out[at] = *reinterpret_cast<const uint16_t*>(&b);
-  } else {
-    p.out[at] = __half_as_ushort(__float2half_rn(v));
-  }
-  if (p.lse && ch == 0)
-    p.lse[static_cast<int64_t>(hq) * p.total_tokens + tok] =
-        l != 0.0f ? (m + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
 }
 
 template <int D, bool BF16, bool INT8>
@@ -760,8 +590,7 @@ cudaError_t launch_one(PagedArgs a, cudaStream_t stream) {
   const int rows = static_cast<int>(
       min(static_cast<long long>(kRows),
           static_cast<long long>(a.max_q_len) * a.group));
-  merge_kernel<D, BF16><<<dim3(kGridMax, rows), D, 0, stream>>>(a, kGridMax);
-  return cudaGetLastError();
+  return launch_merge<D, BF16, kRows, 4, 1>(a, kGridMax, rows, stream);
 }
 
 template <int D>
@@ -776,21 +605,14 @@ cudaError_t launch_d(const PagedArgs& a, const PagedShape& s,
 
 }  // namespace
 
-size_t paged_workspace_bytes(int head_dim) {
-  return static_cast<size_t>(2 * kGridMax) *
-         (kRows * (head_dim + 2) * sizeof(float) + 2 * sizeof(int4));
-}
-
-// Workspace: headers first, then the partial rows.
-void paged_step_carve(PagedArgs& a, void* workspace) {
-  a.head = static_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(a.head + 4 * kGridMax);
+size_t paged_step_workspace_bytes(int head_dim) {
+  return workspace_of(kGridMax, kRows, head_dim);
 }
 
 cudaError_t launch_paged_step(const PagedArgs& args, const PagedShape& s,
                               void* workspace, cudaStream_t stream) {
   PagedArgs a = args;
-  paged_step_carve(a, workspace);
+  carve_workspace(a, workspace, kGridMax);
   return s.head_dim == 128 ? launch_d<128>(a, s, stream)
                            : launch_d<64>(a, s, stream);
 }

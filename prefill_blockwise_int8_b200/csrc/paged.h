@@ -51,7 +51,6 @@ cudaError_t launch_rope(const RopeArgs& a, bool bf16, int mode,
 // parameter.
 struct PagedArgs {
   CUtensorMap tm_k, tm_v;  // {d, page_size, hkv, num_pages}
-  CUtensorMap tm_q;        // chunk kernel: {d, hq, T}
   const uint16_t* q;
   int64_t q_st, q_sh;
   const float* k_scale;
@@ -68,8 +67,7 @@ struct PagedArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  // Partial results: slot s of a block holds `rows` rows of {O[d], m, l};
-  // one header per slot says which item it belongs to.
+  // partial results (paged_common.cuh)
   float* part;
   int4* head;
 };
@@ -79,11 +77,14 @@ struct PagedShape {
   bool bf16, int8;
 };
 
-// Blocks of the step kernel's grid and rows of its query tiles; the
-// workspace is sized from these alone.
-size_t paged_workspace_bytes(int head_dim);
+// The step kernel (up to 16 packed rows a pass) and the chunk kernel (256);
+// each has its own workspace size.
+size_t paged_step_workspace_bytes(int head_dim);
+size_t paged_chunk_workspace_bytes(int head_dim);
 
 cudaError_t launch_paged_step(const PagedArgs& a, const PagedShape& s,
                               void* workspace, cudaStream_t stream);
+cudaError_t launch_paged_chunk(const PagedArgs& a, const PagedShape& s,
+                               void* workspace, cudaStream_t stream);
 
 }  // namespace tilemix

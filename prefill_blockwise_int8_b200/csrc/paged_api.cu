@@ -97,6 +97,12 @@ tilemix_status check_heads(const char* where, int hq, int hkv) {
   return ok();
 }
 
+// Which attention kernel: the step kernel reads the cache once per 16 packed
+// rows, the chunk kernel once per 256.
+bool use_step(int max_q_len, int group) {
+  return static_cast<long long>(max_q_len) * group <= 16;
+}
+
 // {d, page_size, hkv, num_pages} map over a page array.
 bool make_pages_map(CUtensorMap* m, const void* base, bool int8, bool bf16,
                     int d, int page_size, int hkv, int num_pages,
@@ -350,7 +356,9 @@ size_t tilemix_attn_paged_workspace_bytes(int max_q_len, int hq, int hkv,
   if (max_q_len < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq / hkv > 128 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return tilemix::paged_workspace_bytes(head_dim);
+  return use_step(max_q_len, hq / hkv)
+             ? tilemix::paged_step_workspace_bytes(head_dim)
+             : tilemix::paged_chunk_workspace_bytes(head_dim);
 }
 
 tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
@@ -404,7 +412,8 @@ tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
   memset(&p, 0, sizeof(p));
   const CUtensorMapSwizzle sw = int8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                 : CU_TENSOR_MAP_SWIZZLE_128B;
-  const int box = 16;
+  const bool step = use_step(a->max_q_len, a->hq / a->hkv);
+  const int box = step ? 16 : a->page_size < 128 ? a->page_size : 128;
   if (!make_pages_map(&p.tm_k, a->k_pages, int8, bf16, d, a->page_size, a->hkv,
                       a->num_pages, a->page_stride, a->token_stride,
                       a->head_stride, box, sw) ||
@@ -439,7 +448,9 @@ tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
   p.lse = a->lse;
   p.status = a->status;
   const tilemix::PagedShape shape{d, bf16, int8};
-  const cudaError_t e = tilemix::launch_paged_step(p, shape, a->workspace, stream);
+  const cudaError_t e =
+      step ? tilemix::launch_paged_step(p, shape, a->workspace, stream)
+           : tilemix::launch_paged_chunk(p, shape, a->workspace, stream);
   if (e != cudaSuccess)
     return fail(TILEMIX_ERR_CUDA, "%s launch: %s", where, cudaGetErrorString(e));
   return ok();

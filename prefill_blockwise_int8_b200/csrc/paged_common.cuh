@@ -1,23 +1,25 @@
 // Device helpers of the paged attention kernels: problem geometry, the split
-// of all key work over the grid, partial results.
+// of all key work over the grid, partial results and their merge.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
 #include "internal.h"
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace tilemix {
 
-// One sequence as the kernels see it.  Packed row r of the sequence and a KV
-// head is query head r % group of new token r / group.
+// One sequence as the kernels see it.
 struct SeqGeom {
   int start, n, len;  // first token row, new tokens, keys
 };
 
 // Sequence b; n = 0 when it has no new tokens or fails a check (reported
-// once per block that looks at it when `report`).
+// when `report`).
 __device__ __forceinline__ SeqGeom seq_geom(const PagedArgs& p, int b,
                                             bool report) {
   const int start = p.cu_seqlens[b];
@@ -38,6 +40,358 @@ __device__ __forceinline__ SeqGeom seq_geom(const PagedArgs& p, int b,
 __device__ __forceinline__ int keys_of_token(const PagedArgs& p,
                                              const SeqGeom& g, int i) {
   return p.causal ? max(0, g.len - g.n + i + 1) : g.len;
+}
+
+// An item of work (a sequence, a KV head and a tile of at most R packed rows
+// of them) and a unit of U keys in it.
+struct Cursor {
+  int b, kvh, qt, unit;
+};
+
+__device__ __forceinline__ bool same_item(const Cursor& a, const Cursor& b) {
+  return a.qt == b.qt && a.kvh == b.kvh && a.b == b.b;
+}
+
+// The line of all items.  A tile packs whole tokens (tpt of them, each with
+// the `group` query heads of the KV head; row = token * group + head) or,
+// for a group above R, one token's heads in `hs` parts.  An item weighs its
+// keys plus kItemKeys for what it costs to begin and end one; every block
+// takes an equal part of the line, cut at units of U keys, so the split
+// follows from the lengths alone.
+template <int R, int U>
+struct Line {
+  static constexpr int kItemKeys = U / 2;
+  int tpt, hs;
+
+  __device__ __forceinline__ explicit Line(const PagedArgs& p)
+      : tpt(max(1, R / p.group)), hs((p.group + R - 1) / R) {}
+
+  __device__ __forceinline__ int blocks(const SeqGeom& g) const {
+    return (g.n + tpt - 1) / tpt;
+  }
+  __device__ __forceinline__ int tiles(const SeqGeom& g) const {
+    return blocks(g) * hs;
+  }
+  // keys of the tile's last row
+  __device__ __forceinline__ int keys(const PagedArgs& p, const SeqGeom& g,
+                                      int qt) const {
+    return keys_of_token(p, g, min((qt / hs + 1) * tpt, g.n) - 1);
+  }
+  __device__ __forceinline__ int units(const PagedArgs& p, const SeqGeom& g,
+                                       int qt) const {
+    return max(1, (keys(p, g, qt) + U - 1) / U);
+  }
+  __device__ __forceinline__ int first_token(int qt) const {
+    return qt / hs * tpt;
+  }
+  __device__ __forceinline__ int first_head(int qt) const {
+    return qt % hs * R;
+  }
+  __device__ __forceinline__ int rows(const PagedArgs& p, const SeqGeom& g,
+                                      int qt) const {
+    return hs > 1 ? min(R, p.group - first_head(qt))
+                  : min(tpt, g.n - first_token(qt)) * p.group;
+  }
+  // Weight of the first k token blocks of one KV head.
+  __device__ __forceinline__ long long prefix(const PagedArgs& p,
+                                              const SeqGeom& g, int k) const {
+    const long long fixed = static_cast<long long>(k) * kItemKeys;
+    if (!p.causal) return hs * (fixed + static_cast<long long>(k) * g.len);
+    const int nb = blocks(g);
+    const long long base = g.len - g.n;
+    const long long full = k < nb ? k : k - 1;  // blocks of tpt tokens
+    // block j (from 1) has base + j tpt keys, none while that is negative
+    const long long none = base < 0 ? min(full, -base / tpt) : 0;
+    const long long m = full - none;
+    const long long sum =
+        m * base + tpt * (m * (full + none + 1) / 2) + (k == nb && k > 0 ? g.len : 0);
+    return hs * (fixed + sum);
+  }
+
+  // Weight of all sequences, by all lanes of a warp.
+  __device__ __forceinline__ long long total(const PagedArgs& p, int lane,
+                                             bool report) const {
+    long long s = 0;
+    for (int b = lane; b < p.batch; b += 32) {
+      const SeqGeom g = seq_geom(p, b, report);
+      s += prefix(p, g, blocks(g)) * p.hkv;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+
+  // The item and unit at position w of the line; {batch, 0, 0, 0} at its end.
+  __device__ __forceinline__ Cursor locate(const PagedArgs& p, long long w,
+                                           int lane) const {
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      long long per_head = 0;
+      if (b < p.batch) {
+        const SeqGeom g = seq_geom(p, b, false);
+        per_head = prefix(p, g, blocks(g));
+      }
+      const long long mine = per_head * p.hkv;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, incl > w);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        long long rem = w - __shfl_sync(0xffffffffu, incl - mine, l);
+        const long long ph = __shfl_sync(0xffffffffu, per_head, l);
+        Cursor c;
+        c.b = b0 + l;
+        c.kvh = static_cast<int>(rem / ph);
+        rem -= c.kvh * ph;
+        const SeqGeom g = seq_geom(p, c.b, false);
+        int lo = 0, hi = blocks(g);  // prefix(lo) <= rem < prefix(hi)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (prefix(p, g, mid) <= rem) lo = mid;
+          else hi = mid;
+        }
+        rem -= prefix(p, g, lo);
+        const int wi = kItemKeys + keys(p, g, lo * hs);
+        const int part = static_cast<int>(rem / wi);
+        c.qt = lo * hs + part;
+        rem -= static_cast<long long>(part) * wi;
+        c.unit = rem <= kItemKeys ? 0 : static_cast<int>(rem - kItemKeys) / U;
+        return c;
+      }
+      w -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return Cursor{p.batch, 0, 0, 0};
+  }
+
+  // The first unit of the next item ({batch, 0, 0, 0} after the last).
+  __device__ __forceinline__ Cursor next(const PagedArgs& p, const SeqGeom& g,
+                                         Cursor c) const {
+    c.unit = 0;
+    if (++c.qt < tiles(g)) return c;
+    c.qt = 0;
+    if (++c.kvh < p.hkv) return c;
+    c.kvh = 0;
+    do {
+      ++c.b;
+    } while (c.b < p.batch && seq_geom(p, c.b, false).n == 0);
+    return c;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Partial results.  Slot 2 c: the item that began in an earlier block and
+// goes on in (or ends with) block c; slot 2 c + 1: the item that begins in
+// block c and goes on.  A slot holds R rows of {O[D] unnormalised, max (base
+// 2), sum, -, -} and a header {used, the item ends here, bad, rows} {first
+// token row, first query head, group, -}.
+// ---------------------------------------------------------------------------
+
+template <int D>
+constexpr int kPartStride = D + 4;  // floats of a row
+
+template <int D, int R>
+__device__ __forceinline__ float* part_row(const PagedArgs& p, int slot,
+                                           int row) {
+  return p.part + (static_cast<size_t>(slot) * R + row) * kPartStride<D>;
+}
+
+__device__ __forceinline__ void clear_headers(const PagedArgs& p) {
+  if (threadIdx.x < 2)
+    p.head[2 * (2 * blockIdx.x + threadIdx.x)] = make_int4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void pdl_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return pack_half2(lo, hi);
+}
+
+// ln of 2^m l; -inf where nothing was summed.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l != 0.0f ? (m + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
+}
+
+constexpr float kNone = -__builtin_huge_valf();  // maximum of no keys
+
+// Running maximum m, sum l and output o of key ranges, added as
+// m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), o likewise.
+template <int V>
+struct Acc {
+  float m, l, o[V];
+  __device__ __forceinline__ void clear() {
+    m = kNone;
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.0f;
+  }
+  __device__ __forceinline__ void add(float mb, float lb, const float (&ob)[V]) {
+    const float mn = fmaxf(m, mb);
+    const float mz = mn == kNone ? 0.0f : mn;
+    const float fa = ex2_approx(m - mz), fb = ex2_approx(mb - mz);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = o[i] * fa + ob[i] * fb;
+    l = l * fa + lb * fb;
+    m = mn;
+  }
+};
+
+// Adds the partial results of the item that begins in block blockIdx.x and
+// goes on in the next ones, in key order.  W warps share a row (each takes
+// every W-th piece); a block of W * rows-per-block warps starts at row
+// blockIdx.y * rows-per-block.  Bound by the latency of three dependent
+// loads (headers, statistics and rows); rows of up to four pieces are in
+// flight at once.
+template <int D, bool BF16, int R, int W, int ROWS>
+__global__ void __launch_bounds__(32 * W * ROWS)
+    paged_merge_kernel(const __grid_constant__ PagedArgs p, int blocks) {
+  constexpr int V = D / 32;  // channels of a lane
+  __shared__ float s_acc[W > 1 ? W * ROWS : 1][D + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+  const int r = blockIdx.y * ROWS + warp / W;
+  const int wr = warp % W;
+  pdl_wait();
+  const int4 h = p.head[2 * (2 * c + 1)];
+  if (!h.x || blockIdx.y * ROWS >= h.w) return;
+  const int4 it = p.head[2 * (2 * c + 1) + 1];
+  Acc<V> acc;
+  acc.clear();
+  bool bad = h.z != 0, done = false;
+  auto load = [&](int slot, float& m, float& l, float (&o)[V]) {
+    const float* x = part_row<D, R>(p, slot, r);
+    m = x[D];
+    l = x[D + 1];
+    if (V == 4) {
+      const float4 v = reinterpret_cast<const float4*>(x)[lane];
+      o[0] = v.x, o[1] = v.y, o[V > 2 ? 2 : 0] = v.z, o[V > 3 ? 3 : 0] = v.w;
+    } else {
+      const float2 v = reinterpret_cast<const float2*>(x)[lane];
+      o[0] = v.x, o[1] = v.y;
+    }
+  };
+  const bool row = r < h.w;
+  if (row && wr == 0) {
+    float m, l, o[V];
+    load(2 * c + 1, m, l, o);
+    acc.add(m, l, o);
+  }
+  int k = 1;  // pieces seen
+  for (int b0 = c + 1; b0 < blocks && !done; b0 += 32) {
+    int4 n = make_int4(0, 0, 0, 0);
+    if (b0 + lane < blocks) n = p.head[4 * (b0 + lane)];
+    unsigned used = __ballot_sync(0xffffffffu, n.x != 0);
+    const unsigned ends = __ballot_sync(0xffffffffu, n.x != 0 && n.y != 0);
+    const unsigned bads = __ballot_sync(0xffffffffu, n.x != 0 && n.z != 0);
+    if (ends) {
+      used &= 0xffffffffu >> (32 - __ffs(ends));
+      done = true;
+    }
+    bad |= (bads & used) != 0;
+    while (used) {
+      float m[4], l[4], o[4][V];
+      int got = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // this warp's next piece
+        int bit = -1;
+        while (used) {
+          const int t = __ffs(used) - 1;
+          used &= used - 1;
+          if (k++ % W == wr) {
+            bit = t;
+            break;
+          }
+        }
+        if (bit >= 0 && row) {
+          load(2 * (b0 + bit), m[j], l[j], o[j]);
+          got = j + 1;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < got) acc.add(m[j], l[j], o[j]);
+    }
+  }
+  if (W > 1) {
+    float* s = s_acc[warp];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[lane * V + i] = acc.o[i];
+    if (lane == 0) {
+      s[D] = acc.m;
+      s[D + 1] = acc.l;
+    }
+    __syncthreads();
+    if (wr != 0) return;
+    for (int w = 1; w < W; ++w) {
+      const float* t = s_acc[warp + w];
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = t[lane * V + i];
+      acc.add(t[D], t[D + 1], o);
+    }
+  }
+  if (bad || !done || !row) return;
+  const int tok = it.x + r / it.z;
+  const int hq = it.y + r % it.z;
+  const float il = 1.0f / acc.l;
+  uint32_t out[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i)
+    out[i] = acc.l == 0.0f
+                 ? 0u
+                 : pack_pair<BF16>(acc.o[2 * i] * il, acc.o[2 * i + 1] * il);
+  uint16_t* dst = p.out + (static_cast<int64_t>(tok) * p.hq + hq) * D;
+  if (V == 4)
+    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(out[0], out[V / 2 - 1]);
+  else
+    reinterpret_cast<uint32_t*>(dst)[lane] = out[0];
+  if (p.lse && lane == 0)
+    p.lse[static_cast<int64_t>(hq) * p.total_tokens + tok] = lse_of(acc.m, acc.l);
+}
+
+// Launches the merge behind `blocks` blocks of an attention kernel on the
+// same stream (it may be scheduled while that kernel drains).
+template <int D, bool BF16, int R, int W, int ROWS>
+cudaError_t launch_merge(const PagedArgs& a, int blocks, int rows,
+                         cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, (rows + ROWS - 1) / ROWS);
+  cfg.blockDim = dim3(32 * W * ROWS);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, BF16, R, W, ROWS>, a,
+                            blocks);
+}
+
+// Workspace: headers first, then the partial rows.
+inline void carve_workspace(PagedArgs& a, void* workspace, int blocks) {
+  a.head = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(a.head + 4 * blocks);
+}
+
+constexpr size_t workspace_of(int blocks, int rows, int head_dim) {
+  return static_cast<size_t>(2 * blocks) *
+         (static_cast<size_t>(rows) * (head_dim + 4) * sizeof(float) +
+          2 * sizeof(int4));
 }
 
 }  // namespace tilemix
