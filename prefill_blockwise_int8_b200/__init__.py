@@ -27,6 +27,8 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import struct as _struct
 from pathlib import Path
 
 __all__ = [
@@ -215,13 +217,13 @@ def _load() -> C.CDLL:
         i32, i32, C.c_double, C.c_double, C.c_double, C.c_double, i32,
         C.POINTER(C.c_double), C.POINTER(C.c_float)]
     lib.tilemix_rope.restype = i32
-    lib.tilemix_rope.argtypes = [C.POINTER(RopeParams), vp]
+    lib.tilemix_rope.argtypes = [vp, vp]  # packed parameter structs
     lib.tilemix_paged_append.restype = i32
-    lib.tilemix_paged_append.argtypes = [C.POINTER(AppendParams), vp]
+    lib.tilemix_paged_append.argtypes = [vp, vp]
     lib.tilemix_attn_paged_workspace_bytes.restype = C.c_size_t
     lib.tilemix_attn_paged_workspace_bytes.argtypes = [i32] * 4
     lib.tilemix_attn_paged.restype = i32
-    lib.tilemix_attn_paged.argtypes = [C.POINTER(AttnPagedParams), vp]
+    lib.tilemix_attn_paged.argtypes = [vp, vp]
     lib.tilemix_status_string.restype = C.c_char_p
     lib.tilemix_status_string.argtypes = [i32]
     lib.tilemix_last_error.restype = C.c_char_p
@@ -257,7 +259,9 @@ class _Lazy:
                 self._lib = _load()
             except (OSError, AttributeError, ImportError) as e:
                 self._lib = _Missing(e)
-        return getattr(self._lib, name)
+        fn = getattr(self._lib, name)
+        self.__dict__[name] = fn  # the next access is a plain attribute's
+        return fn
 
 
 lib = _Lazy()
@@ -265,7 +269,9 @@ lib = _Lazy()
 
 def reload_library():
     """Load libtilemix.so now (again, after a build); raises if unusable."""
-    lib._lib = _load()
+    loaded = _load()
+    lib.__dict__.clear()
+    lib._lib = loaded
     return lib
 
 
@@ -568,43 +574,51 @@ def tilemix_attn_prefill(q, k, v, cu_seqlens, max_seqlen: int, *, q8=None,
 # rotary positions and the paged KV cache
 # ----------------------------------------------------------------------------
 
-class _On:
-    """The device and stream of a call: every tensor has to lie on the device
-    of the first one, which becomes current; without `stream` its current
-    stream is used.  Tensors made inside belong to that stream."""
+def _packer(struct):
+    """Packs a parameter struct from its fields in order (a small call spends
+    less host time here than in setting ctypes fields one by one)."""
+    code = {C.c_uint32: "I", C.c_int: "i", C.c_void_p: "P", C.c_int64: "q",
+            C.c_float: "f", C.c_size_t: "N"}
+    layout = _struct.Struct("@" + "".join(code[t] for _, t in struct._fields_) +
+                            "0q")
+    assert layout.size == C.sizeof(struct)
+    return functools.partial(layout.pack, layout.size)
 
-    def __init__(self, stream, **tensors):
-        torch = _torch()
-        dev = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
+
+_pack_rope = _packer(RopeParams)
+_pack_append = _packer(AppendParams)
+_pack_attn = _packer(AttnPagedParams)
+
+
+def _check_device(index, **tensors):
+    """Every tensor has to lie on GPU `index`."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
             if not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, not on {dev}")
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, not on {dev}")
-        self.device, self.handle = dev, stream.cuda_stream
-        self._stream = stream
-        self._ctx = None
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
-    def __enter__(self):
-        torch = _torch()
-        # entering the current stream again costs host time and does nothing
-        if (self.device.index != torch.cuda.current_device() or
-                self._stream != torch.cuda.current_stream()):
-            self._ctx = torch.cuda.stream(self._stream)
-            self._ctx.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _on(index, stream):
+    """What makes GPU `index` and `stream` (None: that GPU's current stream)
+    current, or None where they are already: tensors made in a call belong to
+    the stream that uses them."""
+    torch = _torch()
+    if index < 0:
+        raise ValueError("the first argument must be a CUDA tensor")
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return None
+        return torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, not on cuda:{index}")
+    return torch.cuda.stream(stream)
+
+
+def _call(fn, where, packed, index):
+    rc = fn(packed, _torch()._C._cuda_getCurrentRawStream(index))
+    if rc != 0:
+        _check(rc, where)
 
 
 def _dtype_code(t, name):
@@ -616,35 +630,47 @@ def _dtype_code(t, name):
     raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
 
 
-def _rows(t, name, shape=None, dtype=None):
+def _rows(t, name, shape, dtype):
     """Token and head strides of a [T, heads, d] tensor (an axis of one
     counts as packed, whatever stride torch gives it)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got "
                          f"{tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, d = t.shape
-    if d > 1 and t.stride(2) != 1:
+    n, h, d = shape
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1:
         raise ValueError(f"{name} must have contiguous channels")
-    sh = t.stride(1) if h > 1 else d
-    return (t.stride(0) if n > 1 else h * sh), sh
+    if h <= 1:
+        sh = d
+    return (st if n > 1 else h * sh), sh
+
+
+def _tokens(t, name):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    return t.shape
 
 
 def _vector(t, name, n, dtype):
-    _dev(t, name, dtype)
-    if t is not None and t.numel() != n:
+    """Pointer of a contiguous vector of n elements."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
-    return t
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _status_word(status):
-    """The caller's status word (int32, at least one element)."""
-    _dev(status, "status", _torch().int32)
-    if status is not None and status.numel() < 1:
+def _status_ptr(status):
+    """Pointer of the caller's status word (int32, at least one element)."""
+    if status is None:
+        return 0
+    if status.numel() < 1:
         raise ValueError("status must hold at least one element")
+    return _vector(status, "status", status.numel(), _torch().int32)
 
 
 def _layout_code(layout):
@@ -652,67 +678,65 @@ def _layout_code(layout):
 
 
 def _frequencies(freqs, head_dim):
-    """Rotated channels of a frequency vector."""
-    if freqs is None:
-        return 0
-    _dev(freqs, "freqs", _torch().float64)
-    if not 0 < 2 * freqs.numel() <= head_dim:
-        raise ValueError(f"freqs must have 1 .. head_dim / 2 elements, got "
-                         f"{freqs.numel()}")
-    return 2 * freqs.numel()
+    """Pointer and rotated channels of a frequency vector."""
+    n = freqs.numel()
+    if not 0 < 2 * n <= head_dim:
+        raise ValueError(f"freqs must have 1 .. head_dim / 2 elements, got {n}")
+    return _vector(freqs, "freqs", n, _torch().float64), 2 * n
 
 
-def _set_cache(p, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
-               kv_lens, status, dtype):
-    """Checks the cache arguments and fills their fields of `p`."""
+def _cache(k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
+           dtype):
+    """Checks the cache arguments: (kv_format, page strides, scale pointers,
+    table stride, batch, page array's shape, table width)."""
     torch = _torch()
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be [num_pages, page_size, hkv, head_dim]")
-    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    shape = k_pages.shape
+    if v_pages.shape != shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("k_pages and v_pages must share shape and dtype")
-    n, page, hkv, d = k_pages.shape
+    n, page, hkv, d = shape
     int8 = k_pages.dtype == torch.int8
     if not int8 and k_pages.dtype != dtype:
         raise ValueError(f"pages must be {dtype} or int8, got {k_pages.dtype}")
-    strides = []
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if d > 1 and t.stride(3) != 1:
-            raise ValueError(f"{name} must have contiguous channels")
-        th = t.stride(2) if hkv > 1 else d
-        tt = t.stride(1) if page > 1 else hkv * th
-        strides.append((t.stride(0) if n > 1 else page * tt, tt, th))
-    if strides[0] != strides[1]:
+    strides = k_pages.stride()
+    if v_pages.stride() != strides:
         raise ValueError("k_pages and v_pages must share their strides")
+    sp, st, sh, sd = strides
+    if sd != 1 and d > 1:
+        raise ValueError("pages must have contiguous channels")
+    if hkv <= 1:
+        sh = d
+    if page <= 1:
+        st = hkv * sh
+    if n <= 1:
+        sp = page * st
     if int8 != (k_scale is not None) or int8 != (v_scale is not None):
         raise ValueError("k_scale and v_scale go with int8 pages, and only "
                          "with them")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _dev(t, name, torch.float32)
-        if t is not None and tuple(t.shape) != (n, hkv, page):
-            raise ValueError(f"{name} must have shape {(n, hkv, page)}, got "
-                             f"{tuple(t.shape)}")
-    if cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must have batch + 1 elements")
+    ks = vs = 0
+    if int8:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.shape != (n, hkv, page):
+                raise ValueError(f"{name} must have shape {(n, hkv, page)}, "
+                                 f"got {tuple(t.shape)}")
+        ks = _vector(k_scale, "k_scale", n * hkv * page, torch.float32)
+        vs = _vector(v_scale, "v_scale", n * hkv * page, torch.float32)
     batch = cu_seqlens.numel() - 1
-    _dev(cu_seqlens, "cu_seqlens", torch.int32)
-    _vector(kv_lens, "kv_lens", batch, torch.int32)
+    if batch < 0:
+        raise ValueError("cu_seqlens must have batch + 1 elements")
     if (page_table.dim() != 2 or page_table.shape[0] != batch or
             page_table.dtype != torch.int32):
         raise ValueError(f"page_table must be int32 [{batch}, max_pages]")
     width = page_table.shape[1]
-    if width > 1 and page_table.stride(1) != 1:
+    ts, tw = page_table.stride()
+    if width > 1 and tw != 1:
         raise ValueError("page_table must have contiguous rows")
-    _status_word(status)
-    p.kv_format = KV_INT8 if int8 else KV_FP16
-    p.k_pages, p.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
-    p.page_stride, p.token_stride, p.head_stride = strides[0]
-    p.k_scale, p.v_scale = _ptr(k_scale), _ptr(v_scale)
-    p.page_table = page_table.data_ptr()
-    p.table_stride = page_table.stride(0) if batch > 1 else width
-    p.cu_seqlens, p.kv_lens = cu_seqlens.data_ptr(), kv_lens.data_ptr()
-    p.batch, p.num_pages, p.page_size, p.max_pages = batch, n, page, width
-    p.hkv, p.head_dim = hkv, d
-    p.status = _ptr(status)
+    return (KV_INT8 if int8 else KV_FP16, sp, st, sh, ks, vs,
+            page_table.data_ptr(), ts if batch > 1 else width,
+            _vector(cu_seqlens, "cu_seqlens", batch + 1, torch.int32),
+            _vector(kv_lens, "kv_lens", batch, torch.int32), batch, n, page,
+            hkv, d, width)
 
 
 def tilemix_rope_frequencies(rot_dim: int, base: float = 10000.0, *,
@@ -746,38 +770,49 @@ def tilemix_rope(q, k, positions, freqs, *, layout="half",
     default to new contiguous tensors; q_out=q rotates in place.
     Returns (q_out, k_out)."""
     torch = _torch()
-    with _On(stream, q=q, k=k, positions=positions, freqs=freqs, q_out=q_out,
-             k_out=k_out) as on:
-        p = RopeParams()
-        p.struct_size = C.sizeof(RopeParams)
-        p.dtype = _dtype_code(q, "q")
-        p.q_stride_t, p.q_stride_h = _rows(q, "q")
-        t, hq, d = q.shape
-        _vector(positions, "positions", t, torch.int32)
-        p.rot_dim = _frequencies(freqs, d)
-        if q_out is None:
-            q_out = torch.empty((t, hq, d), dtype=q.dtype, device=on.device)
-        p.q_out_stride_t, p.q_out_stride_h = _rows(q_out, "q_out", q.shape,
-                                                   q.dtype)
-        if k is not None:
-            if k.dim() != 3 or k.shape[0] != t or k.shape[2] != d:
-                raise ValueError("q and k must share tokens and head_dim")
-            p.k_stride_t, p.k_stride_h = _rows(k, "k", None, q.dtype)
-            p.hkv = k.shape[1]
-            if k_out is None:
-                k_out = torch.empty(tuple(k.shape), dtype=q.dtype,
-                                    device=on.device)
-            p.k_out_stride_t, p.k_out_stride_h = _rows(k_out, "k_out", k.shape,
-                                                       q.dtype)
-            p.k, p.k_out = k.data_ptr(), k_out.data_ptr()
-        elif k_out is not None:
-            raise ValueError("k_out without k")
-        p.layout, p.inverse = _layout_code(layout), int(bool(inverse))
-        p.q, p.q_out = q.data_ptr(), q_out.data_ptr()
-        p.positions, p.freqs = positions.data_ptr(), freqs.data_ptr()
-        p.attn_factor = attn_factor
-        p.total_tokens, p.hq, p.head_dim = t, hq, d
-        _check(lib.tilemix_rope(C.byref(p), on.handle), "tilemix_rope")
+    index = q.get_device()
+    ctx = _on(index, stream)
+    if ctx is not None:
+        with ctx:
+            return tilemix_rope(q, k, positions, freqs, layout=layout,
+                                attn_factor=attn_factor, inverse=inverse,
+                                q_out=q_out, k_out=k_out)
+    _check_device(index, k=k, positions=positions, freqs=freqs, q_out=q_out,
+                  k_out=k_out)
+    dtype = q.dtype
+    code = _dtype_code(q, "q")
+    shape = _tokens(q, "q")
+    t, hq, d = shape
+    qt, qh = _rows(q, "q", shape, dtype)
+    pos = _vector(positions, "positions", t, torch.int32)
+    fp, rot = _frequencies(freqs, d)
+    if q_out is None:
+        q_out = q.new_empty(shape)
+        qot, qoh = hq * d, d
+    else:
+        qot, qoh = _rows(q_out, "q_out", shape, dtype)
+    kp = kop = hkv = kt = kh = kot = koh = 0
+    if k is not None:
+        kshape = _tokens(k, "k")
+        _, hkv, _ = kshape
+        if kshape[0] != t or kshape[2] != d:
+            raise ValueError("q and k must share tokens and head_dim")
+        kt, kh = _rows(k, "k", kshape, dtype)
+        if k_out is None:
+            k_out = k.new_empty(kshape)
+            kot, koh = hkv * d, d
+        else:
+            kot, koh = _rows(k_out, "k_out", kshape, dtype)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        if t and not (kp and hkv):
+            raise ValueError("k has no heads")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _call(lib.tilemix_rope, "tilemix_rope",
+          _pack_rope(code, _layout_code(layout), 1 if inverse else 0,
+                     q.data_ptr(), kp, q_out.data_ptr(), kop, qt, qh, kt, kh,
+                     qot, qoh, kot, koh, pos, fp, attn_factor, t, hq, hkv, d,
+                     rot), index)
     return q_out, k_out
 
 
@@ -794,46 +829,65 @@ def tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
     position in the cache or by `positions`.  Returns the rotated q (rows
     past cu_seqlens[-1] are not written) or None."""
     torch = _torch()
-    with _On(stream, k=k, v=v, page_table=page_table, cu_seqlens=cu_seqlens,
-             kv_lens=kv_lens, k_pages=k_pages, v_pages=v_pages,
-             k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
-             positions=positions, freqs=freqs, status=status) as on:
-        p = AppendParams()
-        p.struct_size = C.sizeof(AppendParams)
-        p.dtype = _dtype_code(k, "k")
-        _set_cache(p, k_pages, v_pages, k_scale, v_scale, page_table,
-                   cu_seqlens, kv_lens, status, k.dtype)
-        p.k_stride_t, p.k_stride_h = _rows(k, "k")
-        t, hkv, d = k.shape
-        if (hkv, d) != (p.hkv, p.head_dim):
-            raise ValueError("k and the pages must share heads and head_dim")
-        p.v_stride_t, p.v_stride_h = _rows(v, "v", k.shape, k.dtype)
-        p.rot_dim = _frequencies(freqs, d)
-        if freqs is None and (q is not None or positions is not None):
-            raise ValueError("q and positions need freqs")
-        if positions is not None:
-            _vector(positions, "positions", t, torch.int32)
-        if q is not None:
-            if q.dim() != 3 or q.shape[0] != t or q.shape[2] != d:
-                raise ValueError("q and k must share tokens and head_dim")
-            p.q_stride_t, p.q_stride_h = _rows(q, "q", None, k.dtype)
-            if q_out is None:
-                q_out = torch.empty(tuple(q.shape), dtype=k.dtype,
-                                    device=on.device)
-            p.q_out_stride_t, p.q_out_stride_h = _rows(q_out, "q_out", q.shape,
-                                                       k.dtype)
-            p.hq, p.q, p.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        p.layout = _layout_code(layout)
-        p.k, p.v = k.data_ptr(), v.data_ptr()
-        p.positions, p.freqs = _ptr(positions), _ptr(freqs)
-        p.attn_factor, p.total_tokens = attn_factor, t
-        _check(lib.tilemix_paged_append(C.byref(p), on.handle),
-               "tilemix_paged_append")
+    index = k.get_device()
+    ctx = _on(index, stream)
+    if ctx is not None:
+        with ctx:
+            return tilemix_paged_append(
+                k, v, page_table, cu_seqlens, kv_lens, k_pages, v_pages,
+                k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
+                positions=positions, freqs=freqs, layout=layout,
+                attn_factor=attn_factor, status=status)
+    _check_device(index, v=v, page_table=page_table, cu_seqlens=cu_seqlens,
+                  kv_lens=kv_lens, k_pages=k_pages, v_pages=v_pages,
+                  k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
+                  positions=positions, freqs=freqs, status=status)
+    dtype = k.dtype
+    code = _dtype_code(k, "k")
+    (fmt, sp, st, sh, ks, vs, table, ts, cu, lens, batch, n, page, hkv, d,
+     width) = _cache(k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
+                     kv_lens, dtype)
+    shape = _tokens(k, "k")
+    t = shape[0]
+    if shape[1:] != (hkv, d):
+        raise ValueError("k and the pages must share heads and head_dim")
+    kt, kh = _rows(k, "k", shape, dtype)
+    vt, vh = _rows(v, "v", shape, dtype)
+    fp = rot = pos = 0
+    if freqs is not None:
+        fp, rot = _frequencies(freqs, d)
+    elif q is not None or positions is not None:
+        raise ValueError("q and positions need freqs")
+    if positions is not None:
+        pos = _vector(positions, "positions", t, torch.int32)
+    qp = qop = hq = qt = qh = qot = qoh = 0
+    if q is not None:
+        qshape = _tokens(q, "q")
+        hq = qshape[1]
+        if qshape[0] != t or qshape[2] != d:
+            raise ValueError("q and k must share tokens and head_dim")
+        qt, qh = _rows(q, "q", qshape, dtype)
+        if q_out is None:
+            q_out = q.new_empty(qshape)
+            qot, qoh = hq * d, d
+        else:
+            qot, qoh = _rows(q_out, "q_out", qshape, dtype)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+        if t and not qp:
+            raise ValueError("q has no heads")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _call(lib.tilemix_paged_append, "tilemix_paged_append",
+          _pack_append(code, fmt, _layout_code(layout), k.data_ptr(),
+                       v.data_ptr(), qp, qop, kt, kh, vt, vh, qt, qh, qot, qoh,
+                       pos, fp, k_pages.data_ptr(), v_pages.data_ptr(), sp, st,
+                       sh, ks, vs, table, ts, cu, lens, batch, t, hq, hkv, d,
+                       rot, n, page, width, attn_factor, _status_ptr(status)),
+          index)
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def tilemix_attn_paged_workspace_bytes(max_q_len: int, hq: int, hkv: int,
                                        head_dim: int) -> int:
     """Bytes of device scratch tilemix_attn_paged needs."""
@@ -854,36 +908,46 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
     calls that may run at the same time need two.  Rows of q past
     cu_seqlens[-1] are neither read nor written.  Returns out [T, hq, d]."""
     torch = _torch()
-    with _On(stream, q=q, k_pages=k_pages, v_pages=v_pages,
-             page_table=page_table, cu_seqlens=cu_seqlens, kv_lens=kv_lens,
-             k_scale=k_scale, v_scale=v_scale, out=out, lse=lse,
-             workspace=workspace, status=status) as on:
-        p = AttnPagedParams()
-        p.struct_size = C.sizeof(AttnPagedParams)
-        p.dtype = _dtype_code(q, "q")
-        _set_cache(p, k_pages, v_pages, k_scale, v_scale, page_table,
-                   cu_seqlens, kv_lens, status, q.dtype)
-        p.q_stride_t, p.q_stride_h = _rows(q, "q")
-        t, hq, d = q.shape
-        if d != p.head_dim:
-            raise ValueError("q and the pages must share head_dim")
-        if out is None:
-            out = torch.empty((t, hq, d), dtype=q.dtype, device=on.device)
-        _dev(out, "out", q.dtype)
-        if tuple(out.shape) != (t, hq, d):
-            raise ValueError(f"out must have shape {(t, hq, d)}")
-        _vector(lse, "lse", hq * t, torch.float32)
-        if workspace is None:
-            need = tilemix_attn_paged_workspace_bytes(max_q_len, hq, p.hkv, d)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8,
-                                    device=on.device)
-        _dev(workspace, "workspace")
-        p.q, p.out, p.lse = q.data_ptr(), out.data_ptr(), _ptr(lse)
-        p.workspace = workspace.data_ptr()
-        p.workspace_bytes = workspace.numel() * workspace.element_size()
-        p.causal, p.softmax_scale = int(bool(causal)), softmax_scale
-        p.total_tokens, p.hq = t, hq
-        p.max_q_len, p.max_kv_len = max_q_len, max_kv_len
-        _check(lib.tilemix_attn_paged(C.byref(p), on.handle),
-               "tilemix_attn_paged")
+    index = q.get_device()
+    ctx = _on(index, stream)
+    if ctx is not None:
+        with ctx:
+            return tilemix_attn_paged(
+                q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
+                max_q_len, max_kv_len, k_scale=k_scale, v_scale=v_scale,
+                causal=causal, softmax_scale=softmax_scale, out=out, lse=lse,
+                workspace=workspace, status=status)
+    _check_device(index, k_pages=k_pages, v_pages=v_pages,
+                  page_table=page_table, cu_seqlens=cu_seqlens,
+                  kv_lens=kv_lens, k_scale=k_scale, v_scale=v_scale, out=out,
+                  lse=lse, workspace=workspace, status=status)
+    dtype = q.dtype
+    code = _dtype_code(q, "q")
+    (fmt, sp, st, sh, ks, vs, table, ts, cu, lens, batch, n, page, hkv, d,
+     width) = _cache(k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
+                     kv_lens, dtype)
+    shape = _tokens(q, "q")
+    t, hq, dq = shape
+    if dq != d:
+        raise ValueError("q and the pages must share head_dim")
+    qt, qh = _rows(q, "q", shape, dtype)
+    if out is None:
+        out = q.new_empty(shape)
+    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape "
+                         f"{tuple(shape)}")
+    lp = 0 if lse is None else _vector(lse, "lse", hq * t, torch.float32)
+    if workspace is None:
+        need = tilemix_attn_paged_workspace_bytes(max_q_len, hq, hkv, d)
+        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _call(lib.tilemix_attn_paged, "tilemix_attn_paged",
+          _pack_attn(code, fmt, 1 if causal else 0, q.data_ptr(), qt, qh,
+                     k_pages.data_ptr(), v_pages.data_ptr(), sp, st, sh, ks, vs,
+                     table, ts, cu, lens, batch, t, max_q_len, max_kv_len, hq,
+                     hkv, d, n, page, width, softmax_scale, out.data_ptr(), lp,
+                     workspace.data_ptr(),
+                     workspace.numel() * workspace.element_size(),
+                     _status_ptr(status)), index)
     return out

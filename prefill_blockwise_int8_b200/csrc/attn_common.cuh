@@ -73,6 +73,20 @@ __device__ __forceinline__ void i8x4_to_h2x2(uint32_t w, uint32_t& lo,
   hi = *reinterpret_cast<uint32_t*>(&hb);
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
 // Four int8 codes -> two bf16 pairs, exactly: |low 7 bits| under the bf16
 // exponent of 128 minus 128 or, for a set sign bit, minus 256.
 __device__ __forceinline__ void i8x4_to_bf2x2(uint32_t w, uint32_t& lo,

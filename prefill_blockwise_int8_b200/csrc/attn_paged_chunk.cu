@@ -21,12 +21,13 @@
 //               when a maximum moves, and finish O / l;
 //   warp 8      TMA producer: pages through {64 channels, page} boxes into
 //               one ring of K and V tiles (INT8: raw tiles and scales);
-//   warp 9      issues tcgen05.mma: S_t = Q_t K^T and O_t += P_t V with P_t
-//               in TMEM, in the order PV_0, S_0, PV_1, S_1, so one tile's
-//               softmax runs while the other's products do; clears the rows
-//               of the last V tile behind the sequence's end;
+//   warps 9, 10 issue tcgen05.mma of one query tile each: S_t = Q_t K^T of 64 keys a step, two
+//               steps ahead of the softmax, and O_t += P_t V with P_t in
+//               TMEM; clears the rows of the last V tile behind the
+//               sequence's end;
 //   warps 12-15 (INT8) convert raw tiles to 16-bit ones.
-// TMEM: S_0 O_0 S_1 O_1, 128 columns each; P_t over the first 64 of S_t.
+// TMEM per query tile: two S buffers of 64 columns, O in 128; P over the
+// first 32 columns of its S.
 #include <cuda.h>
 
 #include "attn_common.cuh"
@@ -37,7 +38,8 @@ namespace {
 
 constexpr int kM = 128;       // rows of a query tile = TMEM lanes
 constexpr int kRows = 2 * kM; // packed rows of an item
-constexpr int kN = 128;       // keys of a unit
+constexpr int kN = 128;       // keys of a unit and of a K or V tile
+constexpr int kStep = 64;     // keys of a softmax step
 constexpr int kGridMax = 148;
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpConv = 12;
 constexpr int kScRing = 4;    // tiles whose INT8 scales are kept
@@ -67,17 +69,17 @@ struct Cfg {
   static constexpr int kBarOff = kBadOff + 4 * kBadRing;
   // barriers
   static constexpr int kBarQ = 0;                    // [tile]
-  static constexpr int kBarS = 2;                    // [tile]
-  static constexpr int kBarP = 4;                    // [tile][half]
-  static constexpr int kBarO = 8;                    // [tile]
-  static constexpr int kBarFull = 10;                // [slot]
+  static constexpr int kBarS = 2;                    // [tile][buffer]
+  static constexpr int kBarP = 6;                    // [tile][buffer]
+  static constexpr int kBarO = 10;                   // [tile][step parity]
+  static constexpr int kBarFull = 14;                // [slot]
   static constexpr int kBarEmpty = kBarFull + kSlots;
   static constexpr int kBarRawFull = kBarEmpty + kSlots;
   static constexpr int kBarRawEmpty = kBarRawFull + kRawSlots;
   static constexpr int kBarKsc = kBarRawEmpty + kRawSlots;  // [kScRing]
   static constexpr int kBarVsc = kBarKsc + (INT8 ? kScRing : 0);
   static constexpr int kBarDrain = kBarVsc + (INT8 ? kScRing : 0);
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kSmem = kBarOff + 8 * kNumBars + 16 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kBarOff % 8 == 0, "barrier alignment");
@@ -89,6 +91,7 @@ struct Segment {
   int kvh, ua, ub, units;
   int nrows, tok0, head0;
   int keys;   // of the item's last row
+  int steps;  // of kStep keys (the last tile may have one only)
   int index;  // segments before it
 };
 
@@ -113,6 +116,7 @@ __device__ __forceinline__ void for_segments(const PagedArgs& p,
       s.tok0 = line.first_token(cur.qt);
       s.head0 = cur.kvh * p.group + line.first_head(cur.qt);
       s.keys = line.keys(p, s.g, cur.qt);
+      s.steps = min(2 * s.ub, max(1, (s.keys + kStep - 1) / kStep)) - 2 * s.ua;
       s.index = index++;
       if (!f(s, cur.b)) return;
     }
@@ -177,14 +181,16 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
   if (warp == kWarpProducer && lane == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars[C::kBarQ + t], 4);  // one arrival per softmax warp
-      mbar_init(&bars[C::kBarS + t], 1);
+      mbar_init(&bars[C::kBarS + 2 * t], 1);
+      mbar_init(&bars[C::kBarS + 2 * t + 1], 1);
       mbar_init(&bars[C::kBarP + 2 * t], 4);
       mbar_init(&bars[C::kBarP + 2 * t + 1], 4);
-      mbar_init(&bars[C::kBarO + t], 1);
+      mbar_init(&bars[C::kBarO + 2 * t], 1);
+      mbar_init(&bars[C::kBarO + 2 * t + 1], 1);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&bars[C::kBarFull + s], INT8 ? 4 : 1);
-      mbar_init(&bars[C::kBarEmpty + s], 1);
+      mbar_init(&bars[C::kBarEmpty + s], 2);  // both MMA warps
     }
     if (INT8) {
       for (int s = 0; s < C::kRawSlots; ++s) {
@@ -197,6 +203,7 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
       }
     }
     mbar_init(&bars[C::kBarDrain], 1);
+    mbar_init(&bars[C::kBarDrain + 1], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_k);
@@ -298,107 +305,122 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
       if (!ok)
         for (uint32_t i = first; i < idx; ++i)
           mbar_wait(&bars[kFull + i % kStages], (i / kStages) & 1, nullptr);
-    } else if (warp == kWarpMma) {
-      // =================== MMA issuer ===================
+    } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+      // =================== MMA issuers ===================
+      // One warp per query tile: a wait between two products costs about 100
+      // cycles of an idle tensor core (its queue holds little more than the
+      // product it runs), unless the other tile's warp issues meanwhile.
+      const int t = warp - kWarpMma;
       constexpr uint32_t kFmtQ = BF16 ? 1 : 0;
       constexpr uint32_t kFmtP = BF16 && !INT8 ? 1 : 0;
-      constexpr uint32_t id_s = instr_desc(1, kFmtQ, kFmtQ, 0, 0, kN, kM);
+      constexpr uint32_t id_s = instr_desc(1, kFmtQ, kFmtQ, 0, 0, kStep, kM);
       constexpr uint32_t id_o = instr_desc(1, kFmtP, kFmtP, 0, 1, D, kM);
-      const uint64_t dq = desc_k_f16(smem_u32(smem), kM * 128, 0);
+      const uint64_t dq = desc_k_f16(smem_u32(smem + t * C::kQTile), kM * 128, 0);
       const uint64_t dk = desc_k_f16(smem_u32(ring), kN * 128, 0);
       const uint64_t dv = desc_v(smem_u32(ring), kN * 128, 0);
-      uint32_t idx = 0;                 // tiles consumed (K and V count each)
-      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};
+      // Everything that picks a slot, a phase or a descriptor is made warp-
+      // uniform, so the issue path runs on the uniform datapath: with
+      // per-thread values an MMA took 90 cycles to issue, above the 64 it
+      // takes to run.
+      const uint32_t tb = uniform(tmem + t * 256);
+      uint64_t* bar_s = &bars[C::kBarS + 2 * t];
+      uint64_t* bar_o = &bars[C::kBarO + 2 * t];
+      uint32_t base = 0;  // ring tiles of earlier segments
+      uint32_t gs = 0;    // steps so far
+      uint32_t nq = 0;
       bool ok = true;
-      auto issue_s = [&](int t, uint32_t slot) {
-        if (lane == 0) {
-          const uint64_t q = dq + t * (C::kQTile >> 4);
-          const uint64_t k = dk + static_cast<uint64_t>(slot) * (C::kTile >> 4);
+      auto full = [&](uint32_t i) {
+        return ok = wait(C::kBarFull + i % C::kSlots, i / C::kSlots);
+      };
+      auto free_slot = [&](uint32_t i) {
+        if (elect_one()) mma_commit(&bars[C::kBarEmpty + i % C::kSlots]);
+        __syncwarp();
+      };
+      // S of step i (half `half` of the K tile in ring tile r)
+      auto issue_s = [&](uint32_t i, uint32_t r, uint32_t half) {
+        if (elect_one()) {
+          const uint64_t k = dk + (r % C::kSlots) * (C::kTile >> 4) +
+                             half * (kStep * 128 / 16);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t o = (ks >> 2) * (kM * 128 / 16) + k_step(ks);
-            mma_f16_ss(tmem + t * 256, q + o, k + o, id_s, ks > 0 ? 1u : 0u);
+            mma_f16_ss(tb + (i & 1) * kStep, dq + o, k + o, id_s, ks > 0 ? 1u : 0u);
           }
-          mma_commit(&bars[C::kBarS + t]);
+          mma_commit(bar_s + (i & 1));
         }
         __syncwarp();
       };
       for_segments(p, line, begin, end, [&](const Segment& s, int) {
-        const int tiles = s.nrows > kM ? 2 : 1;
-        auto full = [&](uint32_t i) {
-          return ok = wait(C::kBarFull + i % C::kSlots, i / C::kSlots);
-        };
-        auto free_slot = [&](uint32_t i) {
-          if (lane == 0) mma_commit(&bars[C::kBarEmpty + i % C::kSlots]);
-          __syncwarp();
-        };
-        if (!full(idx)) return false;
-        for (int t = 0; t < tiles; ++t) {
-          if (!(ok = wait(C::kBarQ + t, nq[t]++))) return false;
-          tc_fence_after();
-          issue_s(t, idx % C::kSlots);
-        }
-        free_slot(idx);
-        for (int n = s.ua; n < s.ub; ++n) {
-          const uint32_t iv = idx + 1, ik = idx + 2;
-          const bool last = n + 1 == s.ub;
-          const uint32_t vslot = iv % C::kSlots;
-          for (int t = 0; t < tiles; ++t) {
-            if (t == 0) {
-              if (!full(iv)) return false;
-              const int live = s.g.len - n * kN;
-              if (!INT8 && live < kN) {
-                // rows behind the sequence's end may hold anything: P there
-                // is 0, but 0 times NaN is not
-                const int r0 = max(live, 0);
-                for (int c = 0; c < D / 64; ++c) {
-                  uint4* z = reinterpret_cast<uint4*>(ring + vslot * C::kTile +
-                                                      c * (kN * 128) + r0 * 128);
-                  for (int i = lane; i < (kN - r0) * 8; i += 32)
-                    z[i] = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
-            }
-            const uint32_t tb = tmem + t * 256;
-            const uint64_t v = dv + static_cast<uint64_t>(vslot) * (C::kTile >> 4);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!(ok = wait(C::kBarP + 2 * t + h, np[t]))) return false;
-              tc_fence_after();
-              if (lane == 0) {
-#pragma unroll
-                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                  mma_f16_ts(tb + 128, tb + ks * 8, v + ks * (16 * 128 / 16), id_o,
-                             n > s.ua || ks > 0 ? 1u : 0u);
-              }
-              __syncwarp();
-            }
-            ++np[t];
-            if (last) {
-              if (lane == 0) mma_commit(&bars[C::kBarO + t]);
-              __syncwarp();
-            } else {
-              if (t == 0) {
-                if (!full(ik)) return false;
-                tc_fence_after();
-              }
-              issue_s(t, ik % C::kSlots);
-            }
+        const int ua = uniform(s.ua), len = uniform(s.g.len);
+        const int steps = uniform(s.steps);
+        const uint32_t tiles = uniform(s.ub) - ua;
+        if (t * kM >= uniform(s.nrows)) {  // this query tile is empty
+          for (uint32_t i = 0; i < 2 * tiles; ++i) {
+            // (not before the slot is full: its phases stay in order)
+            if (!full(base + i)) return false;
+            free_slot(base + i);
           }
-          free_slot(iv);
-          if (!last) free_slot(ik);
-          idx += 2;
+          base += 2 * tiles;
+          return true;
         }
+        // two steps' scores are made ahead of the softmax
+        if (!full(base)) return false;
+        if (!(ok = wait(C::kBarQ + t, nq++))) return false;
+        tc_fence_after();
+        issue_s(gs, base, 0);
+        if (steps > 1) issue_s(gs + 1, base, 1);
+        free_slot(base);
+        for (int j = 0; j < steps; ++j, ++gs) {
+          const uint32_t half = j & 1;
+          const uint32_t ik = base + ((j + 2) & ~1);  // K tile of step j + 2
+          const uint32_t iv = ik - 1;                 // V tile of step j
+          const bool ahead = j + 2 < steps;
+          if (half == 0) {
+            if (!full(iv)) return false;
+            const int live = len - (ua + (j >> 1)) * kN;
+            if (!INT8 && live < kN) {
+              // rows behind the sequence's end may hold anything: P there is
+              // 0, but 0 times NaN is not (both warps write the same zeros)
+              const int r0 = max(live, 0);
+              for (int c = 0; c < D / 64; ++c) {
+                uint4* z = reinterpret_cast<uint4*>(
+                    ring + (iv % C::kSlots) * C::kTile + c * (kN * 128) + r0 * 128);
+                for (int i = lane; i < (kN - r0) * 8; i += 32)
+                  z[i] = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (ahead && !full(ik)) return false;
+          }
+          // O += P V of step j; S of step j + 2 overwrites P of step j:
+          // products of one thread run in the order they were issued
+          if (!(ok = wait(C::kBarP + 2 * t + (gs & 1), gs >> 1))) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t v = dv + (iv % C::kSlots) * (C::kTile >> 4) +
+                               half * (kStep * 128 / 16);
+#pragma unroll
+            for (int ks = 0; ks < kStep / 16; ++ks)
+              mma_f16_ts(tb + 128, tb + (gs & 1) * kStep + ks * 8,
+                         v + ks * (16 * 128 / 16), id_o, ks > 0 || j > 0 ? 1u : 0u);
+            // (by step parity, as S and P: step gs is not waited for before
+            // step gs - 2 has completed, so a wait cannot mistake the phase)
+            mma_commit(bar_o + (gs & 1));
+          }
+          __syncwarp();
+          if (ahead) issue_s(gs + 2, ik, half);
+          if (half || j + 1 == steps) free_slot(iv);
+          if (ahead && (half || j + 3 == steps)) free_slot(ik);
+        }
+        base += 2 * tiles;
         return true;
       });
       if (!ok) fail();
       // every MMA issued above has finished once this completes
-      if (lane == 0) {
-        mma_commit(&bars[C::kBarDrain]);
-        mbar_wait(&bars[C::kBarDrain], 0, nullptr);
-      }
+      if (elect_one()) mma_commit(&bars[C::kBarDrain + t]);
+      __syncwarp();
+      mbar_wait(&bars[C::kBarDrain + t], 0, nullptr);
       __syncwarp();
     } else if (INT8 && warp >= kWarpConv) {
       // =================== INT8 converters (4 warps) ===================
@@ -468,8 +490,8 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
     const uint32_t ta =
         tmem + t * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint8_t* sq = smem + t * C::kQTile;
-    uint32_t ns = 0, no = 0;  // S tiles and segments seen
-    uint32_t tile = 0;        // tiles of all segments
+    uint32_t gs = 0;    // steps of this query tile so far
+    uint32_t tile = 0;  // key tiles of earlier segments
     bool ok = true;
     for_segments(p, line, begin, end, [&](const Segment& s, int) {
       if (t * kM >= s.nrows) {
@@ -478,12 +500,12 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
       }
       // ---- Q: D/8 threads a row, 16 bytes each ----
       {
-        constexpr int kU = D / 8, kStep = kM / kU;
+        constexpr int kU = D / 8, kRowStep = kM / kU;
         const int u = r % kU;
         uint4 x[kU];
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-          const int row = t * kM + r / kU + k * kStep;
+          const int row = t * kM + r / kU + k * kRowStep;
           x[k] = make_uint4(0, 0, 0, 0);
           if (row < s.nrows)
             x[k] = *reinterpret_cast<const uint4*>(
@@ -492,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-          const int row = r / kU + k * kStep;
+          const int row = r / kU + k * kRowStep;
           *reinterpret_cast<uint4*>(
               sq + swz((u >> 3) * (kM * 128) + row * 128 + (u & 7) * 16, 7)) = x[k];
         }
@@ -508,84 +530,89 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
       const int lim_min = keys_of_token(p, s.g, s.tok0 + t * kM / p.group);
       float m_run = -CUDART_INF_F, l_run = 0.0f;
       float inv = 0.0f;
-      for (int n = s.ua; n < s.ub; ++n, ++tile) {
-        const uint32_t sr = tile % kScRing;
-        if (!wait(C::kBarS + t, ns)) return ok = false;
-        ++ns;
+      for (int j = 0; j < s.steps; ++j, ++gs) {
+        const int key0 = s.ua * kN + j * kStep;
+        const uint32_t kt = tile + (j >> 1);  // key tile, its scales' slot
+        const uint32_t sc_at = (kt % kScRing) * kN + (j & 1) * kStep;
+        const uint32_t sa = ta + (gs & 1) * kStep;
+        if (!wait(C::kBarS + 2 * t + (gs & 1), gs >> 1)) return ok = false;
         tc_fence_after();
-        uint32_t sv[kN];
-        tmem_ld32_at(ta, sv, 0);
-        tmem_ld32_at(ta, sv, 32);
-        tmem_ld32_at(ta, sv, 64);
-        tmem_ld32_at(ta, sv, 96);
-        if (INT8 && !wait(C::kBarKsc + sr, tile / kScRing)) return ok = false;
+        uint32_t sv[kStep];
+        tmem_ld32_at(sa, sv, 0);
+        tmem_ld32_at(sa, sv, 32);
+        if (INT8 && !(j & 1) && !wait(C::kBarKsc + kt % kScRing, kt / kScRing))
+          return ok = false;
         tmem_ld_wait();
         if (INT8) {  // logits: the keys' scales differ
-          const float4* kc = reinterpret_cast<const float4*>(ksc + sr * kN);
+          const uint32_t kc = smem_u32(ksc + sc_at);
 #pragma unroll
-          for (int j = 0; j < kN; j += 4) {
-            const float4 c = kc[j / 4];
-            const float2 a = __fmul2_rn(make_float2(__uint_as_float(sv[j]),
-                                                    __uint_as_float(sv[j + 1])),
-                                        make_float2(c.x, c.y));
-            const float2 b = __fmul2_rn(make_float2(__uint_as_float(sv[j + 2]),
-                                                    __uint_as_float(sv[j + 3])),
-                                        make_float2(c.z, c.w));
-            sv[j] = __float_as_uint(a.x), sv[j + 1] = __float_as_uint(a.y);
-            sv[j + 2] = __float_as_uint(b.x), sv[j + 3] = __float_as_uint(b.y);
+          for (int i = 0; i < kStep; i += 4) {
+            const uint4 w = lds128(kc + 4 * i);
+            const float2 a = __fmul2_rn(
+                make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])),
+                make_float2(__uint_as_float(w.x), __uint_as_float(w.y)));
+            const float2 b = __fmul2_rn(
+                make_float2(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])),
+                make_float2(__uint_as_float(w.z), __uint_as_float(w.w)));
+            sv[i] = __float_as_uint(a.x), sv[i + 1] = __float_as_uint(a.y);
+            sv[i + 2] = __float_as_uint(b.x), sv[i + 3] = __float_as_uint(b.y);
           }
         }
-        if ((n + 1) * kN > lim_min) {  // by position, whatever the slot held
-          const int hl = lim - n * kN;
+        if (key0 + kStep > lim_min) {  // by position, whatever the slot held
+          const int hl = lim - key0;
 #pragma unroll
-          for (int j = 0; j < kN; ++j)
-            if (j >= hl) sv[j] = 0xff800000u;  // -inf
+          for (int i = 0; i < kStep; ++i)
+            if (i >= hl) sv[i] = 0xff800000u;  // -inf
         }
+        // a NaN or +inf score makes the maximum NaN, and with it the row
         float mx;
         {
           float a[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            a[k] = fmaxf(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
+            a[k] = fmax_nan(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
 #pragma unroll
-          for (int j = 16; j < kN; j += 16)
+          for (int i = 16; i < kStep; i += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              a[k] = fmax3(a[k], __uint_as_float(sv[j + 2 * k]),
-                           __uint_as_float(sv[j + 2 * k + 1]));
-          mx = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]),
-                     fmaxf(a[6], a[7]));
+              a[k] = fmax3_nan(a[k], __uint_as_float(sv[i + 2 * k]),
+                               __uint_as_float(sv[i + 2 * k + 1]));
+          mx = fmax3_nan(fmax3_nan(a[0], a[1], a[2]), fmax3_nan(a[3], a[4], a[5]),
+                         fmax_nan(a[6], a[7]));
         }
         const float c = INT8 ? 1.0f : p.scale_log2;
         mx = mx == -CUDART_INF_F ? mx : mx * c;
-        bool need = mx > m_run + kRescaleThreshold;
+        if (mx == CUDART_INF_F) mx = CUDART_NAN_F;
+        bool need = !(mx <= m_run + kRescaleThreshold);
         float alpha = 1.0f;
         if (need) {
           alpha = ex2_approx(m_run - mx);
           m_run = mx;
           l_run *= alpha;
         }
-        float ve = 0.0f;
         if (INT8) {
-          if (!wait(C::kBarVsc + sr, tile / kScRing)) return ok = false;
-          ve = vexp[sr];
+          if (!(j & 1) && !wait(C::kBarVsc + kt % kScRing, kt / kScRing))
+            return ok = false;
+          const float ve = vexp[kt % kScRing];
           if (ve != inv) {
             alpha *= inv == 0.0f ? 0.0f : ve / inv;
             inv = ve;
             need = true;
           }
         }
-        // S_t(n) is ready, so the products before it are done: O_t may be
-        // rescaled now
-        if (n > s.ua && __any_sync(0xffffffffu, need)) {
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+          // the products of the step before have to be done
+          if (!wait(C::kBarO + 2 * t + ((gs - 1) & 1), (gs - 1) >> 1))
+            return ok = false;
+          tc_fence_after();
 #pragma unroll 1
           for (int oc = 0; oc < D; oc += 16) {
             uint32_t o[16];
             tmem_ld16(ta + 128 + oc, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
             tmem_st16(ta + 128 + oc, o);
           }
         }
@@ -594,40 +621,40 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
         float2 ps[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) ps[k] = make_float2(0.f, 0.f);
-        const float4* vc = reinterpret_cast<const float4*>(vsc + sr * kN);
+        const uint32_t vc = smem_u32(vsc + sc_at);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kStep / 32; ++q) {
           uint32_t pk[16];
+          uint4 v4 = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int j = 32 * q + 2 * i;
+            const int k = 32 * q + 2 * i;
             const float2 sc =
-                make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
+                make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]));
             const float2 x = INT8 ? __fadd2_rn(sc, nm) : __ffma2_rn(sc, c2, nm);
             float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             ps[i & 3] = __fadd2_rn(ps[i & 3], e);
             if (INT8) {
-              const float4 v4 = vc[j / 4];
-              e = __fmul2_rn(e, (i & 1) ? make_float2(v4.z, v4.w)
-                                        : make_float2(v4.x, v4.y));
+              if ((i & 1) == 0) v4 = lds128(vc + 4 * k);
+              e = __fmul2_rn(
+                  e, (i & 1) ? make_float2(__uint_as_float(v4.z), __uint_as_float(v4.w))
+                             : make_float2(__uint_as_float(v4.x), __uint_as_float(v4.y)));
             }
             pk[i] = pack_pair<BF16 && !INT8>(e.x, e.y);
           }
-          tmem_st16(ta + 16 * q, pk);
-          if (q & 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[C::kBarP + 2 * t + (q >> 1)]);
-          }
+          tmem_st16(sa + 16 * q, pk);
         }
         const float2 s2 =
             __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
         l_run += s2.x + s2.y;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::kBarP + 2 * t + (gs & 1)]);
       }
+      tile += s.ub - s.ua;
       // ---- O_t / l, or a partial result ----
-      if (!wait(C::kBarO + t, no)) return ok = false;
-      ++no;
+      if (!wait(C::kBarO + 2 * t + ((gs - 1) & 1), (gs - 1) >> 1)) return ok = false;
       tc_fence_after();
       const bool whole = s.ua == 0 && s.ub == s.units;
       const bool bad = bad_ring[s.index % kBadRing] != 0;
