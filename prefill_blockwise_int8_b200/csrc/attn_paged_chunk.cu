@@ -3,11 +3,11 @@
 //
 // Mathematics.  As in the step kernel: the query heads of one KV head and
 // the new tokens pack into rows; per row a running maximum m (base-2 logits,
-// moved lazily: only when a key exceeds it by more than 2^8), sum l and
+// moved lazily, see kLag), sum l and
 // unnormalised output O.  INT8 pages: K codes convert exactly to the query's
 // type and their scale multiplies the fp32 score; V codes convert exactly to
 // fp16 and their scale joins P as P sv 2^-E, 2^E a power of two near the
-// scales seen (raised, with O rescaled, when a scale passes 32 times it), so
+// scales seen (raised, with O rescaled, when a scale passes 16 times it), so
 // that products stay inside fp16's range.
 //
 // B200 design.  One CTA per SM takes an equal part of the line of all items
@@ -45,7 +45,7 @@ constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpConv = 12;
 constexpr int kScRing = 4;    // tiles whose INT8 scales are kept
 constexpr int kBadRing = 8;   // segments whose page check is kept
 
-template <int D, bool INT8>
+template <int D, bool BF16, bool INT8>
 struct Cfg {
   static constexpr int kThreads = INT8 ? 512 : 384;
   // Registers after the split: softmax warps (256 threads) and the others;
@@ -54,6 +54,20 @@ struct Cfg {
   static constexpr int kRegsOther = INT8 ? 72 : 88;
   static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther ==
                 kThreads * (INT8 ? 128 : 168), "register split");
+  // How far (base 2) a row's maximum may pass the reference of its
+  // exponentials before O is rescaled.  A rescale stalls the query tile for
+  // some 1000 cycles, and with a lag of 8 every fourth step of scores with a
+  // spread of 7 had one in some row; P <= 2^15 fits fp16 (INT8: 2^11 times
+  // scales of up to 2^4), and nothing is lost below, where the reference is
+  // never above the maximum.  In bf16 O, 2^24 max |V| keys, stays far inside
+  // fp32.
+  static constexpr float kLag = INT8 ? 11.0f : BF16 ? 24.0f : 15.0f;
+  static constexpr float kScaleLag = 16.0f;
+  // Of eight pairs of exponentials, how many run on the FMA pipe instead of
+  // the exponential unit: 2048 tokens over 32768 keys 956 us with none, 936
+  // with 2, 965 with 3; INT8, whose scales fill the FMA pipe, 530 with none,
+  // 545 with 2.
+  static constexpr int kPolyOf8 = INT8 ? 0 : 2;
   static constexpr int kQTile = kM * D * 2;
   static constexpr int kTile = kN * D * 2;
   static constexpr int kSlots = INT8 ? 3 : D == 128 ? 5 : 8;
@@ -61,8 +75,8 @@ struct Cfg {
   static constexpr int kRawSlots = INT8 ? 3 : 0;
   static constexpr int kRingOff = 2 * kQTile;
   static constexpr int kRawOff = kRingOff + kSlots * kTile;
-  static constexpr int kRawScOff = kRawOff + kRawSlots * kRaw;  // [raw][128]
-  static constexpr int kKscOff = kRawScOff + kRawSlots * kN * 4;
+  static constexpr int kRawScOff = kRawOff + kRawSlots * kRaw;  // [raw][2][128]
+  static constexpr int kKscOff = kRawScOff + kRawSlots * kN * 8;
   static constexpr int kVscOff = kKscOff + (INT8 ? kScRing * kN * 4 : 0);
   static constexpr int kExpOff = kVscOff + (INT8 ? kScRing * kN * 4 : 0);
   static constexpr int kBadOff = kExpOff + 4 * kScRing;
@@ -76,9 +90,8 @@ struct Cfg {
   static constexpr int kBarEmpty = kBarFull + kSlots;
   static constexpr int kBarRawFull = kBarEmpty + kSlots;
   static constexpr int kBarRawEmpty = kBarRawFull + kRawSlots;
-  static constexpr int kBarKsc = kBarRawEmpty + kRawSlots;  // [kScRing]
-  static constexpr int kBarVsc = kBarKsc + (INT8 ? kScRing : 0);
-  static constexpr int kBarDrain = kBarVsc + (INT8 ? kScRing : 0);
+  static constexpr int kBarSc = kBarRawEmpty + kRawSlots;  // [kScRing]
+  static constexpr int kBarDrain = kBarSc + (INT8 ? kScRing : 0);
   static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kSmem = kBarOff + 8 * kNumBars + 16 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
@@ -151,9 +164,9 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst,
 }
 
 template <int D, bool BF16, bool INT8>
-__global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
     chunk_kernel(const __grid_constant__ PagedArgs p) {
-  using C = Cfg<D, INT8>;
+  using C = Cfg<D, BF16, INT8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -198,8 +211,7 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
         mbar_init(&bars[C::kBarRawEmpty + s], 4);
       }
       for (int s = 0; s < kScRing; ++s) {
-        mbar_init(&bars[C::kBarKsc + s], 4);
-        mbar_init(&bars[C::kBarVsc + s], 4);
+        mbar_init(&bars[C::kBarSc + s], 4);
       }
     }
     mbar_init(&bars[C::kBarDrain], 1);
@@ -224,7 +236,9 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
   };
   // warp-wide wait; false once some wait ran out anywhere in the CTA
   auto wait = [&](int bar, uint32_t parity) -> bool {
-    const bool got = mbar_wait(&bars[bar], parity & 1u, abort_flag);
+    parity &= 1u;
+    if (__all_sync(0xffffffffu, mbar_try_wait(&bars[bar], parity))) return true;
+    const bool got = mbar_wait(&bars[bar], parity, abort_flag);
     return __all_sync(0xffffffffu, got);
   };
 
@@ -265,8 +279,7 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
           }
           const int live = min(kN, s.g.len - n * kN);
           const uint32_t pieces = live > 0 ? (live + bt - 1) >> bt_shift : 0;
-          const uint32_t bytes =
-              pieces * bt * (INT8 ? D + 4 : D * 2);
+          const uint32_t bytes = pieces * bt * (INT8 ? D : D * 2);
           const int slot_key = (n * kN + piece * bt) & ((1 << p.page_shift) - 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
@@ -275,7 +288,8 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
               ok = false;
               break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(&bars[kFull + st], bytes);
+            if (lane == 0) mbar_arrive_expect_tx(
+                  &bars[kFull + st], bytes + (INT8 && kv == 0 ? pieces * bt * 8 : 0));
             __syncwarp();
             if (load) {
               const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
@@ -283,11 +297,14 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
               if (INT8) {
                 tma_load_4d(smem + C::kRawOff + st * C::kRaw + piece * bt * D, tm,
                             bar, 0, slot_key, s.kvh, id);
-                const float* sc = kv ? p.v_scale : p.k_scale;
-                bulk_load(smem + C::kRawScOff + (st * kN + piece * bt) * 4,
-                          sc + (((static_cast<int64_t>(id) * p.hkv + s.kvh)
-                                 << p.page_shift) + slot_key),
-                          bt * 4, bar);
+                if (kv == 0) {  // the scales of K and V come with K
+                  const int64_t at =
+                      ((static_cast<int64_t>(id) * p.hkv + s.kvh) << p.page_shift) +
+                      slot_key;
+                  uint8_t* sc = smem + C::kRawScOff + (st * 2 * kN + piece * bt) * 4;
+                  bulk_load(sc, p.k_scale + at, bt * 4, bar);
+                  bulk_load(sc + kN * 4, p.v_scale + at, bt * 4, bar);
+                }
               } else {
                 tma_load_4d(ring + st * C::kTile + chunk * (kN * 128) +
                                 piece * bt * 128,
@@ -332,23 +349,19 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
       auto full = [&](uint32_t i) {
         return ok = wait(C::kBarFull + i % C::kSlots, i / C::kSlots);
       };
-      auto free_slot = [&](uint32_t i) {
-        if (elect_one()) mma_commit(&bars[C::kBarEmpty + i % C::kSlots]);
-        __syncwarp();
-      };
-      // S of step i (half `half` of the K tile in ring tile r)
+      // S of step i (half `half` of the K tile in ring tile r), by one lane
       auto issue_s = [&](uint32_t i, uint32_t r, uint32_t half) {
-        if (elect_one()) {
-          const uint64_t k = dk + (r % C::kSlots) * (C::kTile >> 4) +
-                             half * (kStep * 128 / 16);
+        const uint64_t k = dk + (r % C::kSlots) * (C::kTile >> 4) +
+                           half * (kStep * 128 / 16);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t o = (ks >> 2) * (kM * 128 / 16) + k_step(ks);
-            mma_f16_ss(tb + (i & 1) * kStep, dq + o, k + o, id_s, ks > 0 ? 1u : 0u);
-          }
-          mma_commit(bar_s + (i & 1));
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t o = (ks >> 2) * (kM * 128 / 16) + k_step(ks);
+          mma_f16_ss(tb + (i & 1) * kStep, dq + o, k + o, id_s, ks > 0 ? 1u : 0u);
         }
-        __syncwarp();
+        mma_commit(bar_s + (i & 1));
+      };
+      auto free_slot = [&](uint32_t i) {
+        mma_commit(&bars[C::kBarEmpty + i % C::kSlots]);
       };
       for_segments(p, line, begin, end, [&](const Segment& s, int) {
         const int ua = uniform(s.ua), len = uniform(s.g.len);
@@ -358,7 +371,8 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
           for (uint32_t i = 0; i < 2 * tiles; ++i) {
             // (not before the slot is full: its phases stay in order)
             if (!full(base + i)) return false;
-            free_slot(base + i);
+            if (elect_one()) free_slot(base + i);
+            __syncwarp();
           }
           base += 2 * tiles;
           return true;
@@ -367,37 +381,47 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
         if (!full(base)) return false;
         if (!(ok = wait(C::kBarQ + t, nq++))) return false;
         tc_fence_after();
-        issue_s(gs, base, 0);
-        if (steps > 1) issue_s(gs + 1, base, 1);
-        free_slot(base);
+        if (elect_one()) {
+          issue_s(gs, base, 0);
+          if (steps > 1) issue_s(gs + 1, base, 1);
+          free_slot(base);
+        }
+        __syncwarp();
         for (int j = 0; j < steps; ++j, ++gs) {
           const uint32_t half = j & 1;
           const uint32_t ik = base + ((j + 2) & ~1);  // K tile of step j + 2
           const uint32_t iv = ik - 1;                 // V tile of step j
           const bool ahead = j + 2 < steps;
+          // one vote for all that the step needs, usually there by now
+          bool ready = mbar_try_wait(&bars[C::kBarP + 2 * t + (gs & 1)], (gs >> 1) & 1);
           if (half == 0) {
-            if (!full(iv)) return false;
-            const int live = len - (ua + (j >> 1)) * kN;
-            if (!INT8 && live < kN) {
-              // rows behind the sequence's end may hold anything: P there is
-              // 0, but 0 times NaN is not (both warps write the same zeros)
-              const int r0 = max(live, 0);
-              for (int c = 0; c < D / 64; ++c) {
-                uint4* z = reinterpret_cast<uint4*>(
-                    ring + (iv % C::kSlots) * C::kTile + c * (kN * 128) + r0 * 128);
-                for (int i = lane; i < (kN - r0) * 8; i += 32)
-                  z[i] = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            if (ahead && !full(ik)) return false;
+            ready &= mbar_try_wait(&bars[C::kBarFull + iv % C::kSlots],
+                                   (iv / C::kSlots) & 1);
+            if (ahead)
+              ready &= mbar_try_wait(&bars[C::kBarFull + ik % C::kSlots],
+                                     (ik / C::kSlots) & 1);
           }
-          // O += P V of step j; S of step j + 2 overwrites P of step j:
-          // products of one thread run in the order they were issued
-          if (!(ok = wait(C::kBarP + 2 * t + (gs & 1), gs >> 1))) return false;
+          if (!__all_sync(0xffffffffu, ready)) {
+            if (!(ok = wait(C::kBarP + 2 * t + (gs & 1), gs >> 1))) return false;
+            if (half == 0 && (!full(iv) || (ahead && !full(ik)))) return false;
+          }
+          if (!INT8 && half == 0 && len - (ua + (j >> 1)) * kN < kN) {
+            // rows behind the sequence's end may hold anything: P there is
+            // 0, but 0 times NaN is not (both warps write the same zeros)
+            const int r0 = max(len - (ua + (j >> 1)) * kN, 0);
+            for (int c = 0; c < D / 64; ++c) {
+              uint4* z = reinterpret_cast<uint4*>(
+                  ring + (iv % C::kSlots) * C::kTile + c * (kN * 128) + r0 * 128);
+              for (int i = lane; i < (kN - r0) * 8; i += 32)
+                z[i] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           tc_fence_after();
           if (elect_one()) {
+            // O += P V of step j; S of step j + 2 overwrites P of step j:
+            // products of one thread run in the order they were issued
             const uint64_t v = dv + (iv % C::kSlots) * (C::kTile >> 4) +
                                half * (kStep * 128 / 16);
 #pragma unroll
@@ -407,11 +431,11 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
             // (by step parity, as S and P: step gs is not waited for before
             // step gs - 2 has completed, so a wait cannot mistake the phase)
             mma_commit(bar_o + (gs & 1));
+            if (ahead) issue_s(gs + 2, ik, half);
+            if (half || j + 1 == steps) free_slot(iv);
+            if (ahead && (half || j + 3 == steps)) free_slot(ik);
           }
           __syncwarp();
-          if (ahead) issue_s(gs + 2, ik, half);
-          if (half || j + 1 == steps) free_slot(iv);
-          if (ahead && (half || j + 3 == steps)) free_slot(ik);
         }
         base += 2 * tiles;
         return true;
@@ -442,31 +466,30 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
               return false;
             }
             const float* sc =
-                reinterpret_cast<const float*>(smem + C::kRawScOff) + raw * kN;
+                reinterpret_cast<const float*>(smem + C::kRawScOff) + raw * 2 * kN;
             const int live = s.g.len - n * kN;
             uint8_t* dst = ring + st * C::kTile;
             const uint8_t* src = smem + C::kRawOff + raw * C::kRaw;
             if (kv == 0) {
-              ksc[sr * kN + r] = r < live ? sc[r] * p.scale_log2 : 0.0f;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars[C::kBarKsc + sr]);
-              convert_codes<D, BF16>(src, dst, r);
-            } else {
+              const float* sv = sc + kN;
               float top = 0.0f;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (4 * lane + j < live) top = fmaxf(top, fabsf(sc[4 * lane + j]));
+                if (4 * lane + j < live) top = fmaxf(top, fabsf(sv[4 * lane + j]));
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              if (top > 0.0f && (inv == 0.0f || top * inv > 32.0f)) {
+              if (top > 0.0f && (inv == 0.0f || top * inv > C::kScaleLag)) {
                 const int e = min(max(ilogbf(top) + 1, -126), 126);
                 inv = ldexpf(1.0f, -e);
               }
-              vsc[sr * kN + r] = r < live ? sc[r] * inv : 0.0f;
+              ksc[sr * kN + r] = r < live ? sc[r] * p.scale_log2 : 0.0f;
+              vsc[sr * kN + r] = r < live ? sv[r] * inv : 0.0f;
               if (r == 0) vexp[sr] = inv;
               __syncwarp();
-              if (lane == 0) mbar_arrive(&bars[C::kBarVsc + sr]);
+              if (lane == 0) mbar_arrive(&bars[C::kBarSc + sr]);
+              convert_codes<D, BF16>(src, dst, r);
+            } else {
               // rows behind the end: any code is finite, and P is 0 there
               convert_codes<D, false>(src, dst, r);
             }
@@ -540,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
         uint32_t sv[kStep];
         tmem_ld32_at(sa, sv, 0);
         tmem_ld32_at(sa, sv, 32);
-        if (INT8 && !(j & 1) && !wait(C::kBarKsc + kt % kScRing, kt / kScRing))
+        if (INT8 && !(j & 1) && !wait(C::kBarSc + kt % kScRing, kt / kScRing))
           return ok = false;
         tmem_ld_wait();
         if (INT8) {  // logits: the keys' scales differ
@@ -583,7 +606,7 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
         const float c = INT8 ? 1.0f : p.scale_log2;
         mx = mx == -CUDART_INF_F ? mx : mx * c;
         if (mx == CUDART_INF_F) mx = CUDART_NAN_F;
-        bool need = !(mx <= m_run + kRescaleThreshold);
+        bool need = !(mx <= m_run + C::kLag);
         float alpha = 1.0f;
         if (need) {
           alpha = ex2_approx(m_run - mx);
@@ -591,8 +614,6 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
           l_run *= alpha;
         }
         if (INT8) {
-          if (!(j & 1) && !wait(C::kBarVsc + kt % kScRing, kt / kScRing))
-            return ok = false;
           const float ve = vexp[kt % kScRing];
           if (ve != inv) {
             alpha *= inv == 0.0f ? 0.0f : ve / inv;
@@ -606,14 +627,16 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
             return ok = false;
           tc_fence_after();
 #pragma unroll 1
-          for (int oc = 0; oc < D; oc += 16) {
-            uint32_t o[16];
-            tmem_ld16(ta + 128 + oc, o);
+          for (int oc = 0; oc < D; oc += 64) {
+            uint32_t o[64];
+            tmem_ld32_at(ta + 128 + oc, o, 0);
+            tmem_ld32_at(ta + 128 + oc, o, 32);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 64; ++i)
               o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(ta + 128 + oc, o);
+#pragma unroll
+            for (int i = 0; i < 64; i += 16) tmem_st16(ta + 128 + oc + i, o + i);
           }
         }
         const float mu = m_run == -CUDART_INF_F ? 0.0f : m_run;
@@ -632,7 +655,9 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
             const float2 sc =
                 make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]));
             const float2 x = INT8 ? __fadd2_rn(sc, nm) : __ffma2_rn(sc, c2, nm);
-            float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            float2 e = (i & 7) < C::kPolyOf8
+                           ? ex2_poly2(x)
+                           : make_float2(ex2_approx(x.x), ex2_approx(x.y));
             ps[i & 3] = __fadd2_rn(ps[i & 3], e);
             if (INT8) {
               if ((i & 1) == 0) v4 = lds128(vc + 4 * k);
@@ -724,7 +749,7 @@ __global__ void __launch_bounds__(Cfg<D, INT8>::kThreads, 1)
 
 template <int D, bool BF16, bool INT8>
 cudaError_t launch_one(const PagedArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, INT8>;
+  using C = Cfg<D, BF16, INT8>;
   auto kern = chunk_kernel<D, BF16, INT8>;
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
