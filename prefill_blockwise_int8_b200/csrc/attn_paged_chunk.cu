@@ -94,7 +94,7 @@ struct Cfg {
   static constexpr int kBarDrain = kBarSc + (INT8 ? kScRing : 0);
   static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kSmem = kBarOff + 8 * kNumBars + 16 + 1024;
-  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kSmem + 64 <= 232448, "shared memory");
   static_assert(kBarOff % 8 == 0, "barrier alignment");
 };
 
@@ -115,10 +115,11 @@ __device__ __forceinline__ void for_segments(const PagedArgs& p,
                                              const Line<kRows, kN>& line,
                                              Cursor cur, const Cursor& end,
                                              F&& f) {
+  if (cur.b >= p.batch) return;
+  Segment s;
+  s.g = seq_geom(p, cur.b, false);
   int index = 0;
   while (cur.b < p.batch) {
-    Segment s;
-    s.g = seq_geom(p, cur.b, false);
     const bool at_end = same_item(cur, end);
     s.units = line.units(p, s.g, cur.qt);
     s.ua = cur.unit;
@@ -134,7 +135,7 @@ __device__ __forceinline__ void for_segments(const PagedArgs& p,
       if (!f(s, cur.b)) return;
     }
     if (at_end) return;
-    cur = line.next(p, s.g, cur);
+    line.next(p, s.g, cur);
   }
 }
 
@@ -172,16 +173,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  clear_headers(p);
   const Line<kRows, kN> line(p);
-  const long long total = line.total(p, lane, blockIdx.x == 0 && warp == 0);
-  const long long w0 = total * blockIdx.x / gridDim.x;
-  const long long w1 = total * (blockIdx.x + 1) / gridDim.x;
-  pdl_launch();
-  if (w0 >= w1) return;
-  const Cursor begin = line.locate(p, w0, lane);
-  const Cursor end = line.locate(p, w1, lane);
-
   uint8_t* ring = smem + C::kRingOff;
   float* ksc = reinterpret_cast<float*>(smem + C::kKscOff);
   float* vsc = reinterpret_cast<float*>(smem + C::kVscOff);
@@ -225,10 +217,17 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  clear_headers(p);
+  pdl_launch();
   tc_fence_before();
-  __syncthreads();
+  Cursor begin, end;
+  const bool any = find_part(p, line, warp, lane, begin, end);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!any) {
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    return;
+  }
 
   auto fail = [&]() {
     *abort_flag = 1;

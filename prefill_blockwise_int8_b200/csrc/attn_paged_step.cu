@@ -118,29 +118,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     tma_prefetch_desc(&p.tm_v);
   }
   if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-
   clear_headers(p);
-  const Line<kRows, kUnit> line(p);
-  const long long total = line.total(p, lane, blockIdx.x == 0 && warp == 0);
-  const long long w0 = total * blockIdx.x / gridDim.x;
-  const long long w1 = total * (blockIdx.x + 1) / gridDim.x;
   pdl_launch();
-  if (w0 >= w1) return;
-  Cursor cur = line.locate(p, w0, lane);
-  const Cursor end = line.locate(p, w1, lane);
+  const Line<kRows, kUnit> line(p);
+  Cursor cur, end;
+  if (!find_part(p, line, warp, lane, cur, end) || cur.b >= p.batch) return;
+  SeqGeom g = seq_geom(p, cur.b, false);
   uint32_t issued = 0, consumed = 0;  // ring slots, over all items
   bool dead = false;                  // a wait ran out
 
   while (cur.b < p.batch) {
-    const SeqGeom g = seq_geom(p, cur.b, false);
     const bool at_end = same_item(cur, end);
     const int units = line.units(p, g, cur.qt);
     const int ua = cur.unit;
     const int ub = at_end ? end.unit : units;
     if (ua >= ub) {
       if (at_end) break;
-      cur = line.next(p, g, cur);
+      line.next(p, g, cur);
       continue;
     }
     const int nrows = line.rows(p, g, cur.qt);
@@ -559,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     __syncthreads();
 
     if (at_end) break;
-    cur = line.next(p, g, cur);
+    line.next(p, g, cur);
   }
 }
 

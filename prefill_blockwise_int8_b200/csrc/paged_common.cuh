@@ -108,79 +108,110 @@ struct Line {
     return hs * (fixed + sum);
   }
 
-  // Weight of all sequences, by all lanes of a warp.
-  __device__ __forceinline__ long long total(const PagedArgs& p, int lane,
-                                             bool report) const {
-    long long s = 0;
-    for (int b = lane; b < p.batch; b += 32) {
-      const SeqGeom g = seq_geom(p, b, report);
-      s += prefix(p, g, blocks(g)) * p.hkv;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
-  }
-
-  // The item and unit at position w of the line; {batch, 0, 0, 0} at its end.
-  __device__ __forceinline__ Cursor locate(const PagedArgs& p, long long w,
-                                           int lane) const {
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+  // The item and unit at c / parts of the line, by all lanes of a warp;
+  // {batch, 0, 0, 0} at its end.  `report`: this warp reports bad sequences.
+  __device__ __forceinline__ Cursor locate(const PagedArgs& p, int c, int parts,
+                                           int lane, bool report) const {
+    // weights of one KV head of 32 sequences at a time
+    auto per_head = [&](int b0, bool rep) -> long long {
       const int b = b0 + lane;
-      long long per_head = 0;
-      if (b < p.batch) {
-        const SeqGeom g = seq_geom(p, b, false);
-        per_head = prefix(p, g, blocks(g));
-      }
-      const long long mine = per_head * p.hkv;
-      long long incl = mine;
+      if (b >= p.batch) return 0;
+      const SeqGeom g = seq_geom(p, b, rep);
+      return prefix(p, g, blocks(g));
+    };
+    const long long first = per_head(0, report);
+    long long total = first;
+    for (int b0 = 32; b0 < p.batch; b0 += 32) total += per_head(b0, report);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= p.hkv;
+    // (total < 2^31 tokens x keys x heads, so the products fit)
+    long long w = total * c / parts;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const long long head = b0 == 0 ? first : per_head(b0, false);
+      long long incl = head * p.hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       const unsigned past = __ballot_sync(0xffffffffu, incl > w);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        long long rem = w - __shfl_sync(0xffffffffu, incl - mine, l);
-        const long long ph = __shfl_sync(0xffffffffu, per_head, l);
-        Cursor c;
-        c.b = b0 + l;
-        c.kvh = static_cast<int>(rem / ph);
-        rem -= c.kvh * ph;
-        const SeqGeom g = seq_geom(p, c.b, false);
-        int lo = 0, hi = blocks(g);  // prefix(lo) <= rem < prefix(hi)
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (prefix(p, g, mid) <= rem) lo = mid;
-          else hi = mid;
-        }
-        rem -= prefix(p, g, lo);
-        const int wi = kItemKeys + keys(p, g, lo * hs);
-        const int part = static_cast<int>(rem / wi);
-        c.qt = lo * hs + part;
-        rem -= static_cast<long long>(part) * wi;
-        c.unit = rem <= kItemKeys ? 0 : static_cast<int>(rem - kItemKeys) / U;
-        return c;
+      if (past == 0) {
+        w -= __shfl_sync(0xffffffffu, incl, 31);
+        continue;
       }
-      w -= __shfl_sync(0xffffffffu, incl, 31);
+      const int l = __ffs(past) - 1;
+      const long long ph = __shfl_sync(0xffffffffu, head, l);
+      long long rem = w - (__shfl_sync(0xffffffffu, incl, l) - ph * p.hkv);
+      Cursor at;
+      at.b = b0 + l;
+      // the head: the last whose weights before it are at most rem
+      at.kvh = last_below(0, p.hkv, lane, [&](int k) { return k * ph <= rem; });
+      rem -= at.kvh * ph;
+      const SeqGeom g = seq_geom(p, at.b, false);
+      const int lo = last_below(0, blocks(g), lane,
+                                [&](int k) { return prefix(p, g, k) <= rem; });
+      rem -= prefix(p, g, lo);
+      const int wi = kItemKeys + keys(p, g, lo * hs);
+      const int part = hs > 1 ? static_cast<int>(rem / wi) : 0;
+      at.qt = lo * hs + part;
+      rem -= static_cast<long long>(part) * wi;
+      at.unit = rem <= kItemKeys ? 0 : static_cast<int>(rem - kItemKeys) / U;
+      return at;
     }
     return Cursor{p.batch, 0, 0, 0};
   }
 
-  // The first unit of the next item ({batch, 0, 0, 0} after the last).
-  __device__ __forceinline__ Cursor next(const PagedArgs& p, const SeqGeom& g,
-                                         Cursor c) const {
+  // The largest k in [lo, hi) with f(k), f true at lo and then false from
+  // some k on; a warp tests 32 values at a time.
+  template <class F>
+  __device__ __forceinline__ static int last_below(int lo, int hi, int lane,
+                                                   F&& f) {
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) >> 5;
+      const long long k = lo + static_cast<long long>(lane) * step;
+      const unsigned yes =
+          __ballot_sync(0xffffffffu, k < hi && f(static_cast<int>(k)));
+      lo += (__popc(yes) - 1) * step;
+      hi = min(hi, lo + step);
+    }
+    return lo;
+  }
+
+  // The first unit of the next item ({batch, 0, 0, 0} after the last); `g`
+  // follows.
+  __device__ __forceinline__ void next(const PagedArgs& p, SeqGeom& g,
+                                       Cursor& c) const {
     c.unit = 0;
-    if (++c.qt < tiles(g)) return c;
+    if (++c.qt < tiles(g)) return;
     c.qt = 0;
-    if (++c.kvh < p.hkv) return c;
+    if (++c.kvh < p.hkv) return;
     c.kvh = 0;
-    do {
-      ++c.b;
-    } while (c.b < p.batch && seq_geom(p, c.b, false).n == 0);
-    return c;
+    while (++c.b < p.batch) {
+      g = seq_geom(p, c.b, false);
+      if (g.n != 0) return;
+    }
   }
 };
+
+// A block's part of the line: from its own start to the next block's.  Two
+// warps find them; every thread gets both.  False: nothing to do.
+template <class L>
+__device__ __forceinline__ bool find_part(const PagedArgs& p, const L& line,
+                                          int warp, int lane, Cursor& begin,
+                                          Cursor& end) {
+  __shared__ Cursor s_part[2];
+  if (warp < 2) {
+    const Cursor at = line.locate(p, blockIdx.x + warp, gridDim.x, lane,
+                                  blockIdx.x == 0 && warp == 0);
+    if (lane == 0) s_part[warp] = at;
+  }
+  __syncthreads();
+  begin = s_part[0];
+  end = s_part[1];
+  return !(same_item(begin, end) && begin.unit == end.unit);
+}
 
 // ---------------------------------------------------------------------------
 // Partial results.  Slot 2 c: the item that began in an earlier block and
