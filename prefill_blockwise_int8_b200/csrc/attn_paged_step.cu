@@ -17,13 +17,13 @@
 // subnormals and large ones do not overflow.
 //
 // Work split.  All keys of all (sequence, KV head, 16-row tile) items, in
-// units of 64 keys, form one line; block c takes the c-th equal part of it.
+// units of four groups, form one line; block c takes the c-th equal part of it.
 // An item that one block holds whole is written out; the others leave partial
 // results that the merge kernel adds in key order.  No block waits for
 // another, and the split follows from the lengths alone.
 //
-// What bounds it: HBM.  Each warp owns every fourth 16-key group of a block's
-// part and runs alone (private m, l, O and a private ring of TMA slots, no
+// What bounds it: HBM.  Each warp owns every fourth group of 16 or 32 keys of
+// a block's part and runs alone (private m, l, O and a private ring of TMA slots, no
 // block barrier in the loop), so a block keeps 4 rings of loads in flight.
 // The products are small (two m16n8k16 per key for d = 128, a fifth of the
 // tensor rate at full HBM speed), hence warp-level mma fragments that never
@@ -42,19 +42,27 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;    // packed rows of an item (mma M)
-constexpr int kGroup = 16;   // keys of a ring slot
-constexpr int kUnit = kWarps * kGroup;  // keys of a unit of work
-constexpr int kBlocksPerSm = 2;
-constexpr int kGridMax = 148 * kBlocksPerSm;
+constexpr int kGridMax = 148 * 3;
+
+// Blocks of an SM.  16-bit pages of 128 channels are bound by HBM with two
+// (215 registers a thread); the others by the latency of their own
+// instructions, which a third block hides.
+template <int D, bool INT8>
+constexpr int kBlocksPerSm = D == 64 || INT8 ? 3 : 2;
 
 template <int D, bool INT8>
 struct Cfg {
   static constexpr int kElem = INT8 ? 1 : 2;
+  // Keys of a ring slot: as many as leave two slots of a warp.  With 32 the
+  // maxima, votes and copies of a slot cost half as much per key.
+  static constexpr int kGroup = paged_step_group(D, INT8);
+  static constexpr int kUnit = kWarps * kGroup;  // keys of a unit of work
   static constexpr int kTile = kGroup * D * kElem;  // K or V bytes of a slot
   static constexpr int kScale = INT8 ? 2 * kGroup * 4 : 0;
   static constexpr int kSlot = 2 * kTile;
-  // 24 KB of ring per warp, at most 8 slots
-  static constexpr int kSlots = 24576 / kSlot > 8 ? 8 : 24576 / kSlot;
+  // 24 KB of ring per warp (16 with three blocks), at most 8 slots
+  static constexpr int kBytes = kBlocksPerSm<D, INT8> == 3 ? 16384 : 24576;
+  static constexpr int kSlots = kBytes / kSlot > 8 ? 8 : kBytes / kSlot;
   static constexpr int kRing = kSlots * kSlot;
   static constexpr int kRingAll = kWarps * kRing;
   static constexpr int kScaleOff = kRingAll;
@@ -98,9 +106,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4],
 }
 
 template <int D, bool BF16, bool INT8>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
     step_kernel(const __grid_constant__ PagedArgs p) {
   using C = Cfg<D, INT8>;
+  constexpr int G = C::kGroup;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -120,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (threadIdx.x == 0) s_bad = 0;
   clear_headers(p);
   pdl_launch();
-  const Line<kRows, kUnit> line(p);
+  const Line<kRows, C::kUnit> line(p);
   Cursor cur, end;
   if (!find_part(p, line, warp, lane, cur, end) || cur.b >= p.batch) return;
   SeqGeom g = seq_geom(p, cur.b, false);
@@ -155,19 +164,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                           : nullptr;
     }
 
-    // this warp's 16-key groups of units [ua, ub): i-th at key k0 + 64 i
-    const int k0 = ua * kUnit + warp * kGroup;
-    const int kend = min(keys, ub * kUnit);
-    const int nst = dead || k0 >= kend ? 0 : (kend - k0 + kUnit - 1) / kUnit;
+    // this warp's groups of units [ua, ub): i-th at key k0 + i units
+    const int k0 = ua * C::kUnit + warp * G;
+    const int kend = min(keys, ub * C::kUnit);
+    const int nst = dead || k0 >= kend ? 0 : (kend - k0 + C::kUnit - 1) / C::kUnit;
     const int32_t* trow = p.page_table + cur.b * p.table_stride;
+    // A group comes in pieces of whole pages (one, or two of 16 keys); lane l
+    // holds the page of piece pid_base + l and issues piece l of a group.
+    const int box_shift = min(p.page_shift, G == 32 ? 5 : 4);
+    const int ppg_shift = (G == 32 ? 5 : 4) - box_shift;
     int pid = 0, pid_base = -32;
     bool bad_page = false;
     auto fetch_pids = [&](int base) {
       pid_base = base;
       const int i = base + lane;
+      const long long key = k0 + static_cast<long long>(i >> ppg_shift) * C::kUnit +
+                            ((i & ((1 << ppg_shift) - 1)) << box_shift);
       pid = 0;
-      if (i < nst) {
-        pid = trow[(k0 + static_cast<long long>(i) * kUnit) >> p.page_shift];
+      if (i >> ppg_shift < nst && key < g.len) {
+        pid = trow[key >> p.page_shift];
         if (pid < 0 || pid >= p.num_pages) {
           bad_page = true;
           report_status(p.status, kStatusBadPages);
@@ -176,30 +191,39 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
     };
     auto issue = [&](int i) {
-      if (i - pid_base >= 32) fetch_pids(i);
-      const int id = __shfl_sync(0xffffffffu, pid, i - pid_base);
+      const int first = i << ppg_shift;
+      if (first - pid_base >= 32) fetch_pids(first);
+      const int id = __shfl_sync(0xffffffffu, pid, (first - pid_base + lane) & 31);
       const uint32_t s = issued % C::kSlots;
-      if (lane == 0) {
-        const int slot = (k0 + i * kUnit) & ((1 << p.page_shift) - 1);
+      const int key = k0 + i * C::kUnit + (lane << box_shift);
+      const int live = min(G, g.len - (k0 + i * C::kUnit));
+      const int pieces = (live + (1 << box_shift) - 1) >> box_shift;
+      if (lane == 0)
+        mbar_arrive_expect_tx(&bars[s], (pieces << box_shift) *
+                                            (2 * D * C::kElem + (INT8 ? 8 : 0)));
+      if (G == 32) __syncwarp();
+      if (lane < pieces) {
+        const int slot = key & ((1 << p.page_shift) - 1);
         uint8_t* dst = ring + s * C::kSlot;
-        mbar_arrive_expect_tx(&bars[s], C::kSlot + C::kScale);
         if (INT8) {
+          dst += (lane << box_shift) * D;
           tma_load_4d(dst, &p.tm_k, &bars[s], 0, slot, cur.kvh, id);
           tma_load_4d(dst + C::kTile, &p.tm_v, &bars[s], 0, slot, cur.kvh, id);
           const int64_t at =
               ((static_cast<int64_t>(id) * p.hkv + cur.kvh) << p.page_shift) + slot;
-          bulk_load(scales + s * C::kScale, p.k_scale + at, kGroup * 4, &bars[s]);
-          bulk_load(scales + s * C::kScale + kGroup * 4, p.v_scale + at,
-                    kGroup * 4, &bars[s]);
+          uint8_t* sd = scales + s * C::kScale + (4 * lane << box_shift);
+          bulk_load(sd, p.k_scale + at, 4 << box_shift, &bars[s]);
+          bulk_load(sd + G * 4, p.v_scale + at, 4 << box_shift, &bars[s]);
         } else {
+          dst += (lane << box_shift) * 128;
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(dst + c * kGroup * 128, &p.tm_k, &bars[s], c * 64, slot,
+            tma_load_4d(dst + c * G * 128, &p.tm_k, &bars[s], c * 64, slot, cur.kvh,
+                        id);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(dst + C::kTile + c * G * 128, &p.tm_v, &bars[s], c * 64, slot,
                         cur.kvh, id);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(dst + C::kTile + c * kGroup * 128, &p.tm_v, &bars[s],
-                        c * 64, slot, cur.kvh, id);
         }
       }
       ++issued;
@@ -243,30 +267,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       ++consumed;
       const uint32_t ka = ring_a + s * C::kSlot;
       const uint32_t va = ka + C::kTile;
-      const int key0 = k0 + i * kUnit;
-      float sc[2][4];
+      const int key0 = k0 + i * C::kUnit;
+      // column fragment j holds keys 8 j .. 8 j + 7: this thread's key0 + 8 j
+      // + ca and + cb (INT8 rows are taken in the order 0, 4, 1, 5, 2, 6, 3,
+      // 7, which spreads a quarter warp's 16-byte reads over all banks)
+      constexpr int F = G / 8;
+      const int ca = INT8 ? q4 : 2 * q4, cb = INT8 ? q4 + 4 : 2 * q4 + 1;
+      float sc[F][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < F; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[j][e] = 0.0f;
-      // keys of columns 2 q4 and 2 q4 + 1 of fragment j: key0 + kc[j][.]
-      // (INT8 rows are taken in the order 0, 4, 1, 5, 2, 6, 3, 7, which
-      // spreads a quarter warp's 16-byte reads over all banks)
-      const int ca = INT8 ? q4 : 2 * q4, cb = INT8 ? q4 + 4 : 2 * q4 + 1;
-      float skv[4], svv[4];
       if (INT8) {
-        const uint32_t sa = smem_u32(scales + s * C::kScale);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          skv[2 * j] = __uint_as_float(lds32(sa + (8 * j + ca) * 4));
-          skv[2 * j + 1] = __uint_as_float(lds32(sa + (8 * j + cb) * 4));
-          svv[2 * j] = __uint_as_float(lds32(sa + kGroup * 4 + (8 * j + ca) * 4));
-          svv[2 * j + 1] =
-              __uint_as_float(lds32(sa + kGroup * 4 + (8 * j + cb) * 4));
-        }
         const int kr = (g8 >> 1) | ((g8 & 1) << 2);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < F; ++j)
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             const uint32_t off = (8 * j + kr) * D + 64 * c + 16 * q4;
@@ -286,55 +301,68 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const int kr = (lane & 7) + ((lane >> 4) << 3);
         const int hi = (lane >> 3) & 1;
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t) {
-          const uint32_t off =
-              (t >> 2) * kGroup * 128 + kr * 128 + (t & 3) * 32 + hi * 16;
-          uint32_t b[4];
-          ldm_x4(ka + swz(off, 7u), b);
-          mma16816<BF16>(sc[0], qf[t], b[0], b[1]);
-          mma16816<BF16>(sc[1], qf[t], b[2], b[3]);
-        }
+        for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+          for (int j = 0; j < F; j += 2) {
+            const uint32_t off =
+                (t >> 2) * G * 128 + (8 * j + kr) * 128 + (t & 3) * 32 + hi * 16;
+            uint32_t b[4];
+            ldm_x4(ka + swz(off, 7u), b);
+            mma16816<BF16>(sc[j], qf[t], b[0], b[1]);
+            mma16816<BF16>(sc[j + 1], qf[t], b[2], b[3]);
+          }
       }
       // scores in base-2 logits; masked ones -inf (by position, whatever the
       // slot held)
-      const bool masked = key0 + kGroup > keys_min;
+      const uint32_t sa = smem_u32(scales + s * C::kScale);
       float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[j][e] * p.scale_log2;
-          if (INT8) x *= skv[2 * j + (e & 1)];
-          if (masked && key0 + 8 * j + ((e & 1) ? cb : ca) >= lim[e >> 1])
-            x = -CUDART_INF_F;
-          sc[j][e] = x;
-          mx[e >> 1] = fmaxf(mx[e >> 1], x);
-        }
-      bool grow = false;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        grow |= mx[r] > m[r] + kRescaleThreshold;
-      }
       float svm = 0.0f;
+      const bool masked = key0 + G > keys_min;
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        float ka_ = p.scale_log2, kb_ = p.scale_log2;
+        if (INT8) {
+          ka_ *= __uint_as_float(lds32(sa + (8 * j + ca) * 4));
+          kb_ *= __uint_as_float(lds32(sa + (8 * j + cb) * 4));
+        }
+        sc[j][0] *= ka_, sc[j][2] *= ka_;
+        sc[j][1] *= kb_, sc[j][3] *= kb_;
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + 8 * j + ((e & 1) ? cb : ca) >= lim[e >> 1])
+              sc[j][e] = -CUDART_INF_F;
+        }
+        mx[0] = fmaxf(mx[0], fmaxf(sc[j][0], sc[j][1]));
+        mx[1] = fmaxf(mx[1], fmaxf(sc[j][2], sc[j][3]));
+      }
+      // A quad's maxima only matter when one passes the reference by more
+      // than 2^8; the lanes vote on their own first.
+      bool grow = mx[0] > m[0] + kRescaleThreshold || mx[1] > m[1] + kRescaleThreshold;
       if (INT8) {
-        // slots past the sequence's end may hold anything
-        const int live = g.len - key0;
-        svm = fmaxf(fmaxf(ca < live ? svv[0] : 0.0f, cb < live ? svv[1] : 0.0f),
-                    fmaxf(8 + ca < live ? svv[2] : 0.0f,
-                          8 + cb < live ? svv[3] : 0.0f));
-        svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, 1));
-        svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, 2));
+        // the largest live V scale (slots past the end may hold anything)
+        const float v =
+            lane < G ? __uint_as_float(lds32(sa + G * 4 + 4 * (lane & (G - 1)))) : 0.0f;
+        svm = key0 + lane < g.len ? v : 0.0f;
         grow |= inv == 0.0f ? svm > 0.0f : svm * inv > 32.0f;
       }
       if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        }
         float f = 1.0f;
-        if (INT8 && svm > 0.0f && (inv == 0.0f || svm * inv > 32.0f)) {
-          const int e = min(max(ilogbf(svm) + 1, -126), 126);
-          const float ninv = ldexpf(1.0f, -e);
-          f = inv == 0.0f ? 0.0f : ninv / inv;
-          inv = ninv;
+        if (INT8) {
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1)
+            svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, x));
+          if (svm > 0.0f && (inv == 0.0f || svm * inv > 32.0f)) {
+            const int e = min(max(ilogbf(svm) + 1, -126), 126);
+            const float ninv = ldexpf(1.0f, -e);
+            f = inv == 0.0f ? 0.0f : ninv / inv;
+            inv = ninv;
+          }
         }
         float al[2];
 #pragma unroll
@@ -358,83 +386,92 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       // P; a row that has seen no key keeps m = -inf and P = 0
       const float mu[2] = {m[0] == -CUDART_INF_F ? 0.0f : m[0],
                            m[1] == -CUDART_INF_F ? 0.0f : m[1]};
-      uint32_t pf[4];
+      const bool tail = key0 + G > g.len;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float e4[4];
+      for (int h = 0; h < G / 16; ++h) {
+        uint32_t pf[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          e4[e] = ex2_approx(sc[j][e] - mu[e >> 1]);
-          l[e >> 1] += e4[e];
+        for (int jj = 0; jj < 2; ++jj) {
+          const int j = 2 * h + jj;
+          float va_ = 1.0f, vb_ = 1.0f;
           if (INT8) {
-            const int key = 8 * j + ((e & 1) ? cb : ca);
-            // P = 0 times the scale of a slot past the end must stay 0
-            e4[e] = key0 + key < g.len ? e4[e] * (svv[2 * j + (e & 1)] * inv) : 0.0f;
+            va_ = __uint_as_float(lds32(sa + G * 4 + (8 * j + ca) * 4)) * inv;
+            vb_ = __uint_as_float(lds32(sa + G * 4 + (8 * j + cb) * 4)) * inv;
+            if (tail) {  // P = 0 times the scale of a slot past the end is 0
+              if (key0 + 8 * j + ca >= g.len) va_ = 0.0f;
+              if (key0 + 8 * j + cb >= g.len) vb_ = 0.0f;
+            }
           }
-        }
-        pf[2 * j] = pack_pair<BF16 && !INT8>(e4[0], e4[1]);
-        pf[2 * j + 1] = pack_pair<BF16 && !INT8>(e4[2], e4[3]);
-      }
-      // V rows past the sequence's end may hold NaN: cleared in registers
-      const bool tail = key0 + kGroup > g.len;
-      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-      if (INT8) {
-        // any int8 code is finite: P = 0 is enough
-        // ldmatrix rows in the order of the score columns: row 2q -> q, ...
-        const int r8 = lane & 7;
-        const int kr = ((r8 >> 1) | ((r8 & 1) << 2)) + ((lane >> 3) & 1) * 8;
-        const int hi = lane >> 4;
+          float e4[4];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t b[4];
-          ldm_x4_t(va + swz(kr * D + c * 32 + hi * 16, D == 128 ? 7u : 3u), b);
-          // b[0], b[1]: keys 0-7, 8-15 of 16 channels; b[2], b[3]: the next 16
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = b[2 * h] ^ 0x80808080u, y = b[2 * h + 1] ^ 0x80808080u;
-            const __half2 bias = __float2half2_rn(1152.0f);
-            uint32_t xe = __byte_perm(x, 0x64646464u, 0x4240);
-            uint32_t xo = __byte_perm(x, 0x64646464u, 0x4341);
-            uint32_t ye = __byte_perm(y, 0x64646464u, 0x4240);
-            uint32_t yo = __byte_perm(y, 0x64646464u, 0x4341);
-            auto sub = [&](uint32_t& z) {
-              const __half2 t = __hsub2(*reinterpret_cast<__half2*>(&z), bias);
-              z = *reinterpret_cast<const uint32_t*>(&t);
-            };
-            sub(xe);
-            sub(xo);
-            sub(ye);
-            sub(yo);
-            // even and odd channels of the 16 as two n-tiles
-            mma16816<false>(o[4 * c + 2 * h], pf, xe, ye);
-            mma16816<false>(o[4 * c + 2 * h + 1], pf, xo, yo);
+          for (int e = 0; e < 4; ++e) {
+            e4[e] = ex2_approx(sc[j][e] - mu[e >> 1]);
+            l[e >> 1] += e4[e];
+            if (INT8) e4[e] *= (e & 1) ? vb_ : va_;
           }
+          pf[2 * jj] = pack_pair<BF16 && !INT8>(e4[0], e4[1]);
+          pf[2 * jj + 1] = pack_pair<BF16 && !INT8>(e4[2], e4[3]);
         }
-      } else {
-        if (tail) {
-          const int live = g.len - key0;  // keys 2 q4, + 1, + 8, + 9
-          auto keep = [&](int k) {
-            return (k < live ? 0x0000ffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
-          };
-          keep0 = keep(2 * q4);
-          keep1 = keep(2 * q4 + 8);
-        }
-        const int kr = (lane & 7) + ((lane >> 3) & 1) * 8;
-        const int hi = lane >> 4;
+        if (INT8) {
+          // any int8 code is finite: P = 0 is enough behind the end.
+          // ldmatrix rows in the order of the score columns: row 2q -> q, ...
+          const int r8 = lane & 7;
+          const int kr = 16 * h + ((r8 >> 1) | ((r8 & 1) << 2)) + ((lane >> 3) & 1) * 8;
+          const int hi = lane >> 4;
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t) {
-          const uint32_t off =
-              (t >> 2) * kGroup * 128 + kr * 128 + (t & 3) * 32 + hi * 16;
-          uint32_t b[4];
-          ldm_x4_t(va + swz(off, 7u), b);
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t b[4];
+            ldm_x4_t(va + swz(kr * D + c * 32 + hi * 16, D == 128 ? 7u : 3u), b);
+            // b[0], b[1]: keys 0-7, 8-15 of 16 channels; b[2], b[3]: the next
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t y0 = b[2 * x] ^ 0x80808080u;
+              const uint32_t y1 = b[2 * x + 1] ^ 0x80808080u;
+              const __half2 bias = __float2half2_rn(1152.0f);
+              uint32_t xe = __byte_perm(y0, 0x64646464u, 0x4240);
+              uint32_t xo = __byte_perm(y0, 0x64646464u, 0x4341);
+              uint32_t ye = __byte_perm(y1, 0x64646464u, 0x4240);
+              uint32_t yo = __byte_perm(y1, 0x64646464u, 0x4341);
+              auto sub = [&](uint32_t& z) {
+                const __half2 t = __hsub2(*reinterpret_cast<__half2*>(&z), bias);
+                z = *reinterpret_cast<const uint32_t*>(&t);
+              };
+              sub(xe);
+              sub(xo);
+              sub(ye);
+              sub(yo);
+              // even and odd channels of the 16 as two n-tiles
+              mma16816<false>(o[4 * c + 2 * x], pf, xe, ye);
+              mma16816<false>(o[4 * c + 2 * x + 1], pf, xo, yo);
+            }
+          }
+        } else {
+          // V rows past the sequence's end may hold NaN: cleared in registers
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (tail) {
-            b[0] &= keep0;
-            b[1] &= keep1;
-            b[2] &= keep0;
-            b[3] &= keep1;
+            const int live = g.len - key0 - 16 * h;  // keys 2 q4, + 1, + 8, + 9
+            auto keep = [&](int k) {
+              return (k < live ? 0x0000ffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
+            };
+            keep0 = keep(2 * q4);
+            keep1 = keep(2 * q4 + 8);
           }
-          mma16816<BF16>(o[2 * t], pf, b[0], b[1]);
-          mma16816<BF16>(o[2 * t + 1], pf, b[2], b[3]);
+          const int kr = 16 * h + (lane & 7) + ((lane >> 3) & 1) * 8;
+          const int hi = lane >> 4;
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t) {
+            const uint32_t off = (t >> 2) * G * 128 + kr * 128 + (t & 3) * 32 + hi * 16;
+            uint32_t b[4];
+            ldm_x4_t(va + swz(off, 7u), b);
+            if (tail) {
+              b[0] &= keep0;
+              b[1] &= keep1;
+              b[2] &= keep0;
+              b[3] &= keep1;
+            }
+            mma16816<BF16>(o[2 * t], pf, b[0], b[1]);
+            mma16816<BF16>(o[2 * t + 1], pf, b[2], b[3]);
+          }
         }
       }
       __syncwarp();
@@ -564,13 +601,14 @@ cudaError_t launch_one(PagedArgs a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<kGridMax, kThreads, C::kSmem, stream>>>(a);
+  constexpr int grid = 148 * kBlocksPerSm<D, INT8>;
+  kern<<<grid, kThreads, C::kSmem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int rows = static_cast<int>(
       min(static_cast<long long>(kRows),
           static_cast<long long>(a.max_q_len) * a.group));
-  return launch_merge<D, BF16, kRows, 4, 1>(a, kGridMax, rows, stream);
+  return launch_merge<D, BF16, kRows, 4, 1>(a, grid, rows, stream);
 }
 
 template <int D>

@@ -77,6 +77,11 @@ struct PagedShape {
   bool bf16, int8;
 };
 
+// Keys that one copy of the step kernel's ring brings at most.
+constexpr int paged_step_group(int head_dim, bool int8) {
+  return head_dim == 128 && !int8 ? 16 : 32;
+}
+
 // The step kernel (up to 16 packed rows a pass) and the chunk kernel (256);
 // each has its own workspace size.
 size_t paged_step_workspace_bytes(int head_dim);

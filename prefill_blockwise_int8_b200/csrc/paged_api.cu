@@ -413,7 +413,8 @@ tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
   const CUtensorMapSwizzle sw = int8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                 : CU_TENSOR_MAP_SWIZZLE_128B;
   const bool step = use_step(a->max_q_len, a->hq / a->hkv);
-  const int box = step ? 16 : a->page_size < 128 ? a->page_size : 128;
+  const int most = step ? tilemix::paged_step_group(d, int8) : 128;
+  const int box = a->page_size < most ? a->page_size : most;
   if (!make_pages_map(&p.tm_k, a->k_pages, int8, bf16, d, a->page_size, a->hkv,
                       a->num_pages, a->page_stride, a->token_stride,
                       a->head_stride, box, sw) ||
