@@ -24,6 +24,7 @@ namespace tilemix {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxTokens = 16;  // of a block
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 template <bool BF16>
@@ -102,13 +103,14 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int batch,
 // Where a token's rows go (append): page id and slot, or page < 0.
 struct Place {
   int page, slot, pos;
+  int64_t at, scale_at;  // INT8: head 0's row and scale
 };
 
 template <bool BF16, int MODE>  // 0 rotary, 1 append 16-bit, 2 append INT8
 __global__ void __launch_bounds__(kThreads)
     rope_kernel(const __grid_constant__ RopeArgs p, int tokens_per_block) {
   extern __shared__ float2 cs_all[];  // [tokens_per_block][rot_dim / 2]
-  __shared__ Place place[kThreads / 32];
+  __shared__ Place place[kMaxTokens];
   const int t0 = blockIdx.x * tokens_per_block;
   const int nt = min(tokens_per_block, p.total_tokens - t0);
   const int half = p.rot_dim >> 1;
@@ -116,9 +118,9 @@ __global__ void __launch_bounds__(kThreads)
 
   if (MODE != 0) {
     // one warp per token finds its sequence and checks its place
-    if (warp < nt) {
-      const int t = t0 + warp;
-      Place pl{-1, 0, 0};
+    for (int tt = warp; tt < nt; tt += kThreads / 32) {
+      const int t = t0 + tt;
+      Place pl{-1, 0, 0, 0, 0};
       if (t < p.cu_seqlens[p.batch]) {
         const int b = find_sequence(p.cu_seqlens, p.batch, t, lane);
         const int start = p.cu_seqlens[b], end = p.cu_seqlens[b + 1];
@@ -134,12 +136,14 @@ __global__ void __launch_bounds__(kThreads)
           if (page < 0 || page >= p.num_pages) {
             if (lane == 0) report_status(p.status, kStatusBadPages);
           } else {
-            pl = Place{page, static_cast<int>(pos & ((1 << p.page_shift) - 1)),
-                       static_cast<int>(pos)};
+            const int slot = static_cast<int>(pos & ((1 << p.page_shift) - 1));
+            pl = Place{page, slot, static_cast<int>(pos),
+                       page * p.page_stride + slot * p.token_stride,
+                       (static_cast<int64_t>(page) * p.hk << p.page_shift) + slot};
           }
         }
       }
-      if (lane == 0) place[warp] = pl;
+      if (lane == 0) place[tt] = pl;
     }
     __syncthreads();
   }
@@ -180,82 +184,126 @@ __global__ void __launch_bounds__(kThreads)
     v0 = 2 * u;
     v1 = 2 * u + 1;
   }
-  for (int tt = 0; tt < nt; ++tt) {
-    if (MODE != 0 && place[tt].page < 0) continue;
-    const int64_t t = t0 + tt;
-    const float2* cs = cs_all + tt * half + 8 * u;
-    // Every lane runs the same number of rounds: INT8 rows reduce over lanes.
-    for (int h0 = 0; h0 < heads; h0 += slots) {
-      const int h = h0 + slot0;
-      const bool live = slot0 < slots && h < heads;
-      const bool is_q = h < p.hq, is_v = h >= p.hq + p.hk;
-      const int hl = is_q ? h : is_v ? h - p.hq - p.hk : h - p.hq;
-      const RowTensor in = is_q ? p.q : is_v ? p.v : p.k;
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (live) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(in.p + t * in.st + hl * in.sh);
-        a = src[v0];
-        b = src[v1];
-      }
-      if (rotated && !is_v) {
-        float fa[8], fb[8];
-        unpack8<BF16>(a, fa);
-        unpack8<BF16>(b, fb);
-        turn(fa, fb, cs, p.interleaved != 0);
-        a = pack8<BF16>(fa);
-        b = pack8<BF16>(fb);
-      }
-      if (MODE == 0 || is_q) {
+  if constexpr (MODE != 2) {
+    // Tokens outside, heads inside: a block's reads are neighbours (heads
+    // outside took 1.2 times as long).
+    for (int tt = 0; tt < nt; ++tt) {
+      if (MODE != 0 && place[tt].page < 0) continue;
+      const int64_t t = t0 + tt;
+      const float2* cs = cs_all + tt * half + 8 * u;
+      for (int h0 = 0; h0 < heads; h0 += slots) {
+        const int h = h0 + slot0;
+        const bool live = slot0 < slots && h < heads;
+        const bool is_q = h < p.hq, is_v = h >= p.hq + p.hk;
+        const int hl = is_q ? h : is_v ? h - p.hq - p.hk : h - p.hq;
+        const RowTensor in = is_q ? p.q : is_v ? p.v : p.k;
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
         if (live) {
-          const RowTensor out = is_q ? p.q_out : p.k_out;
-          uint4* dst = reinterpret_cast<uint4*>(out.p + t * out.st + hl * out.sh);
-          dst[v0] = a;
-          dst[v1] = b;
+          const uint4* src =
+              reinterpret_cast<const uint4*>(in.p + t * in.st + hl * in.sh);
+          a = src[v0];
+          b = src[v1];
         }
-        if (MODE != 2) continue;
-      }
-      const int64_t at = place[tt].page * p.page_stride +
-                         place[tt].slot * p.token_stride + hl * p.head_stride;
-      if (MODE == 1) {
+        if (rotated && !is_v) {
+          float fa[8], fb[8];
+          unpack8<BF16>(a, fa);
+          unpack8<BF16>(b, fb);
+          turn(fa, fb, cs, p.interleaved != 0);
+          a = pack8<BF16>(fa);
+          b = pack8<BF16>(fb);
+        }
+        if (MODE == 0 || is_q) {
+          if (live) {
+            const RowTensor out = is_q ? p.q_out : p.k_out;
+            uint4* dst = reinterpret_cast<uint4*>(out.p + t * out.st + hl * out.sh);
+            dst[v0] = a;
+            dst[v1] = b;
+          }
+          continue;
+        }
+        const int64_t at = place[tt].page * p.page_stride +
+                           place[tt].slot * p.token_stride + hl * p.head_stride;
         if (live) {
           uint4* dst = reinterpret_cast<uint4*>(
               static_cast<uint16_t*>(is_v ? p.v_pages : p.k_pages) + at);
           dst[v0] = a;
           dst[v1] = b;
         }
-      } else if (MODE == 2) {
+      }
+    }
+  } else {
+    // INT8 rows are bound by instructions, not by HBM: a thread keeps its head
+    // over the block's tokens, so that addresses cost an addition a token, and
+    // the next token's loads are in flight meanwhile (tokens outside: 208 us
+    // where this takes 174).  Every lane runs the same rounds, since rows
+    // reduce over lanes.
+    for (int h0 = 0; h0 < heads; h0 += slots) {
+      const int h = h0 + slot0;
+      const bool mine = slot0 < slots && h < heads;
+      const bool is_q = h < p.hq, is_v = h >= p.hq + p.hk;
+      const int hl = is_q ? h : is_v ? h - p.hq - p.hk : h - p.hq;
+      const RowTensor in = is_q ? p.q : is_v ? p.v : p.k;
+      const uint16_t* src = in.p + static_cast<int64_t>(t0) * in.st + hl * in.sh;
+      const int64_t head_at = hl * p.head_stride;
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      auto fetch = [&](int tt) {
+        if (mine && tt < nt && place[tt].page >= 0) {
+          const uint4* x = reinterpret_cast<const uint4*>(src + tt * in.st);
+          a = x[v0];
+          b = x[v1];
+        }
+      };
+      fetch(0);
+      for (int tt = 0; tt < nt; ++tt) {
+        const bool live = mine && place[tt].page >= 0;
+        uint4 xa = a, xb = b;
+        fetch(tt + 1);
         float fa[8], fb[8];
-        unpack8<BF16>(a, fa);
-        unpack8<BF16>(b, fb);
+        unpack8<BF16>(xa, fa);
+        unpack8<BF16>(xb, fb);
+        if (rotated && !is_v) {
+          turn(fa, fb, cs_all + tt * half + 8 * u, p.interleaved != 0);
+          xa = pack8<BF16>(fa);
+          xb = pack8<BF16>(fb);
+          unpack8<BF16>(xa, fa);
+          unpack8<BF16>(xb, fb);
+        }
+        if (is_q && live) {
+          uint4* y = reinterpret_cast<uint4*>(p.q_out.p + static_cast<int64_t>(t0 + tt) * p.q_out.st +
+                                              hl * p.q_out.sh);
+          y[v0] = xa;
+          y[v1] = xb;
+        }
         float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          m = fmaxf(m, fmaxf(fabsf(fa[i]), fabsf(fb[i])));
-        // units is 4 or 8 (head_dim 64 or 128): a head's lanes are an
-        // aligned group of that many
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(fa[i]), fabsf(fb[i])));
+        // units is 4 or 8 (head_dim 64 or 128): a head's lanes are an aligned
+        // group of that many
         for (int o = units >> 1; o > 0; o >>= 1)
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (live && !is_q) {
-          const float s = __fdiv_rn(m, 127.0f);
-          const float rcp = m != 0.0f ? __frcp_rn(s) : 0.0f;
+          const float sc = __fdiv_rn(m, 127.0f);
+          const float rcp = m != 0.0f ? __frcp_rn(sc) : 0.0f;
           uint32_t ca[8], cb[8];
-          quant_codes8(fa, s, rcp, ca);
-          quant_codes8(fb, s, rcp, cb);
-          int8_t* row = static_cast<int8_t*>(is_v ? p.v_pages : p.k_pages) + at;
-          *reinterpret_cast<uint2*>(row + v0 * 8) =
-              make_uint2(pack_low_bytes4(ca[0], ca[1], ca[2], ca[3]),
-                         pack_low_bytes4(ca[4], ca[5], ca[6], ca[7]));
-          *reinterpret_cast<uint2*>(row + v1 * 8) =
-              make_uint2(pack_low_bytes4(cb[0], cb[1], cb[2], cb[3]),
-                         pack_low_bytes4(cb[4], cb[5], cb[6], cb[7]));
-          if (u == 0) {
-            const int hkv = p.hk;
-            (is_v ? p.v_scale : p.k_scale)
-                [((static_cast<int64_t>(place[tt].page) * hkv + hl)
-                  << p.page_shift) +
-                 place[tt].slot] = s;
+          quant_codes8(fa, sc, rcp, ca);
+          quant_codes8(fb, sc, rcp, cb);
+          const uint2 ya = make_uint2(pack_low_bytes4(ca[0], ca[1], ca[2], ca[3]),
+                                      pack_low_bytes4(ca[4], ca[5], ca[6], ca[7]));
+          const uint2 yb = make_uint2(pack_low_bytes4(cb[0], cb[1], cb[2], cb[3]),
+                                      pack_low_bytes4(cb[4], cb[5], cb[6], cb[7]));
+          int8_t* row = static_cast<int8_t*>(is_v ? p.v_pages : p.k_pages) +
+                        place[tt].at + head_at;
+          if (v1 == v0 + 1) {
+            *reinterpret_cast<uint4*>(row + v0 * 8) =
+                make_uint4(ya.x, ya.y, yb.x, yb.y);
+          } else {
+            *reinterpret_cast<uint2*>(row + v0 * 8) = ya;
+            *reinterpret_cast<uint2*>(row + v1 * 8) = yb;
           }
+          if (u == 0)
+            (is_v ? p.v_scale
+                  : p.k_scale)[place[tt].scale_at +
+                             (static_cast<int64_t>(hl) << p.page_shift)] = sc;
         }
       }
     }
@@ -264,7 +312,10 @@ __global__ void __launch_bounds__(kThreads)
 
 template <bool BF16, int MODE>
 cudaError_t launch_one(const RopeArgs& a, cudaStream_t stream) {
-  const int tpb = a.total_tokens >= 1024 ? 4 : 1;
+  // few tokens: a block each, so that all SMs work; many: their places and
+  // angles are shared work
+  constexpr int kMany = MODE == 2 ? kMaxTokens : 4;
+  const int tpb = a.total_tokens >= 1024 ? kMany : 1;
   const int grid = (a.total_tokens + tpb - 1) / tpb;
   const size_t smem = a.freqs ? tpb * (a.rot_dim / 2) * sizeof(float2) : 0;
   rope_kernel<BF16, MODE><<<grid, kThreads, smem, stream>>>(a, tpb);
