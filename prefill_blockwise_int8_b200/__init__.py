@@ -590,20 +590,20 @@ _pack_append = _packer(AppendParams)
 _pack_attn = _packer(AttnPagedParams)
 
 
-def _check_device(index, **tensors):
+def _check_device(index, names, *tensors):
     """Every tensor has to lie on GPU `index`."""
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is not None and t.get_device() != index:
+            name = names.split()[i]
             if not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor")
             raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
-def _on(index, stream):
+def _on(torch, index, stream):
     """What makes GPU `index` and `stream` (None: that GPU's current stream)
     current, or None where they are already: tensors made in a call belong to
     the stream that uses them."""
-    torch = _torch()
     if index < 0:
         raise ValueError("the first argument must be a CUDA tensor")
     if stream is None:
@@ -615,19 +615,18 @@ def _on(index, stream):
     return torch.cuda.stream(stream)
 
 
-def _call(fn, where, packed, index):
-    rc = fn(packed, _torch()._C._cuda_getCurrentRawStream(index))
+def _call(torch, fn, where, packed, index):
+    rc = fn(packed, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         _check(rc, where)
 
 
-def _dtype_code(t, name):
-    torch = _torch()
-    if t.dtype == torch.float16:
+def _dtype_code(torch, dtype, name):
+    if dtype is torch.float16:
         return 0
-    if t.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return 1
-    raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    raise ValueError(f"{name} must be float16 or bfloat16, got {dtype}")
 
 
 def _rows(t, name, shape, dtype):
@@ -685,20 +684,20 @@ def _frequencies(freqs, head_dim):
     return _vector(freqs, "freqs", n, _torch().float64), 2 * n
 
 
-def _cache(k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
-           dtype):
+def _cache(torch, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
+           kv_lens, dtype):
     """Checks the cache arguments: (kv_format, page strides, scale pointers,
     table stride, batch, page array's shape, table width)."""
-    torch = _torch()
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be [num_pages, page_size, hkv, head_dim]")
     shape = k_pages.shape
     if v_pages.shape != shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("k_pages and v_pages must share shape and dtype")
     n, page, hkv, d = shape
-    int8 = k_pages.dtype == torch.int8
-    if not int8 and k_pages.dtype != dtype:
-        raise ValueError(f"pages must be {dtype} or int8, got {k_pages.dtype}")
+    kind = k_pages.dtype
+    int8 = kind is torch.int8
+    if not int8 and kind is not dtype:
+        raise ValueError(f"pages must be {dtype} or int8, got {kind}")
     strides = k_pages.stride()
     if v_pages.stride() != strides:
         raise ValueError("k_pages and v_pages must share their strides")
@@ -771,16 +770,16 @@ def tilemix_rope(q, k, positions, freqs, *, layout="half",
     Returns (q_out, k_out)."""
     torch = _torch()
     index = q.get_device()
-    ctx = _on(index, stream)
+    ctx = _on(torch, index, stream)
     if ctx is not None:
         with ctx:
             return tilemix_rope(q, k, positions, freqs, layout=layout,
                                 attn_factor=attn_factor, inverse=inverse,
                                 q_out=q_out, k_out=k_out)
-    _check_device(index, k=k, positions=positions, freqs=freqs, q_out=q_out,
-                  k_out=k_out)
+    _check_device(index, "k positions freqs q_out k_out", k, positions, freqs,
+                  q_out, k_out)
     dtype = q.dtype
-    code = _dtype_code(q, "q")
+    code = _dtype_code(torch, dtype, "q")
     shape = _tokens(q, "q")
     t, hq, d = shape
     qt, qh = _rows(q, "q", shape, dtype)
@@ -808,7 +807,7 @@ def tilemix_rope(q, k, positions, freqs, *, layout="half",
             raise ValueError("k has no heads")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call(lib.tilemix_rope, "tilemix_rope",
+    _call(torch, lib.tilemix_rope, "tilemix_rope",
           _pack_rope(code, _layout_code(layout), 1 if inverse else 0,
                      q.data_ptr(), kp, q_out.data_ptr(), kop, qt, qh, kt, kh,
                      qot, qoh, kot, koh, pos, fp, attn_factor, t, hq, hkv, d,
@@ -830,7 +829,7 @@ def tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
     past cu_seqlens[-1] are not written) or None."""
     torch = _torch()
     index = k.get_device()
-    ctx = _on(index, stream)
+    ctx = _on(torch, index, stream)
     if ctx is not None:
         with ctx:
             return tilemix_paged_append(
@@ -838,15 +837,15 @@ def tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
                 k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
                 positions=positions, freqs=freqs, layout=layout,
                 attn_factor=attn_factor, status=status)
-    _check_device(index, v=v, page_table=page_table, cu_seqlens=cu_seqlens,
-                  kv_lens=kv_lens, k_pages=k_pages, v_pages=v_pages,
-                  k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
-                  positions=positions, freqs=freqs, status=status)
+    _check_device(index, "v page_table cu_seqlens kv_lens k_pages v_pages "
+                  "k_scale v_scale q q_out positions freqs status", v,
+                  page_table, cu_seqlens, kv_lens, k_pages, v_pages, k_scale,
+                  v_scale, q, q_out, positions, freqs, status)
     dtype = k.dtype
-    code = _dtype_code(k, "k")
+    code = _dtype_code(torch, dtype, "k")
     (fmt, sp, st, sh, ks, vs, table, ts, cu, lens, batch, n, page, hkv, d,
-     width) = _cache(k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
-                     kv_lens, dtype)
+     width) = _cache(torch, k_pages, v_pages, k_scale, v_scale, page_table,
+                     cu_seqlens, kv_lens, dtype)
     shape = _tokens(k, "k")
     t = shape[0]
     if shape[1:] != (hkv, d):
@@ -877,7 +876,7 @@ def tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
             raise ValueError("q has no heads")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _call(lib.tilemix_paged_append, "tilemix_paged_append",
+    _call(torch, lib.tilemix_paged_append, "tilemix_paged_append",
           _pack_append(code, fmt, _layout_code(layout), k.data_ptr(),
                        v.data_ptr(), qp, qop, kt, kh, vt, vh, qt, qh, qot, qoh,
                        pos, fp, k_pages.data_ptr(), v_pages.data_ptr(), sp, st,
@@ -909,7 +908,7 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
     cu_seqlens[-1] are neither read nor written.  Returns out [T, hq, d]."""
     torch = _torch()
     index = q.get_device()
-    ctx = _on(index, stream)
+    ctx = _on(torch, index, stream)
     if ctx is not None:
         with ctx:
             return tilemix_attn_paged(
@@ -917,15 +916,15 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
                 max_q_len, max_kv_len, k_scale=k_scale, v_scale=v_scale,
                 causal=causal, softmax_scale=softmax_scale, out=out, lse=lse,
                 workspace=workspace, status=status)
-    _check_device(index, k_pages=k_pages, v_pages=v_pages,
-                  page_table=page_table, cu_seqlens=cu_seqlens,
-                  kv_lens=kv_lens, k_scale=k_scale, v_scale=v_scale, out=out,
-                  lse=lse, workspace=workspace, status=status)
+    _check_device(index, "k_pages v_pages page_table cu_seqlens kv_lens "
+                  "k_scale v_scale out lse workspace status", k_pages, v_pages,
+                  page_table, cu_seqlens, kv_lens, k_scale, v_scale, out, lse,
+                  workspace, status)
     dtype = q.dtype
-    code = _dtype_code(q, "q")
+    code = _dtype_code(torch, dtype, "q")
     (fmt, sp, st, sh, ks, vs, table, ts, cu, lens, batch, n, page, hkv, d,
-     width) = _cache(k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
-                     kv_lens, dtype)
+     width) = _cache(torch, k_pages, v_pages, k_scale, v_scale, page_table,
+                     cu_seqlens, kv_lens, dtype)
     shape = _tokens(q, "q")
     t, hq, dq = shape
     if dq != d:
@@ -942,7 +941,7 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
         workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _call(lib.tilemix_attn_paged, "tilemix_attn_paged",
+    _call(torch, lib.tilemix_attn_paged, "tilemix_attn_paged",
           _pack_attn(code, fmt, 1 if causal else 0, q.data_ptr(), qt, qh,
                      k_pages.data_ptr(), v_pages.data_ptr(), sp, st, sh, ks, vs,
                      table, ts, cu, lens, batch, t, max_q_len, max_kv_len, hq,

@@ -557,19 +557,26 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
         const uint32_t kt = tile + (j >> 1);  // key tile, its scales' slot
         const uint32_t sc_at = (kt % kScRing) * kN + (j & 1) * kStep;
         const uint32_t sa = ta + (gs & 1) * kStep;
+        // INT8: the key scales, fetched before the scores they multiply are
+        // there (one by one beside them, each load's latency showed)
+        uint4 ks[INT8 ? kStep / 4 : 1];
+        if (INT8) {
+          if (!(j & 1) && !wait(C::kBarSc + kt % kScRing, kt / kScRing))
+            return ok = false;
+          const uint32_t kc = smem_u32(ksc + sc_at);
+#pragma unroll
+          for (int i = 0; i < kStep / 4; ++i) ks[i] = lds128(kc + 16 * i);
+        }
         if (!wait(C::kBarS + 2 * t + (gs & 1), gs >> 1)) return ok = false;
         tc_fence_after();
         uint32_t sv[kStep];
         tmem_ld32_at(sa, sv, 0);
         tmem_ld32_at(sa, sv, 32);
-        if (INT8 && !(j & 1) && !wait(C::kBarSc + kt % kScRing, kt / kScRing))
-          return ok = false;
         tmem_ld_wait();
         if (INT8) {  // logits: the keys' scales differ
-          const uint32_t kc = smem_u32(ksc + sc_at);
 #pragma unroll
           for (int i = 0; i < kStep; i += 4) {
-            const uint4 w = lds128(kc + 4 * i);
+            const uint4 w = ks[INT8 ? i / 4 : 0];
             const float2 a = __fmul2_rn(
                 make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])),
                 make_float2(__uint_as_float(w.x), __uint_as_float(w.y)));
@@ -647,7 +654,11 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < kStep / 32; ++q) {
           uint32_t pk[16];
-          uint4 v4 = make_uint4(0, 0, 0, 0);
+          uint4 vs[INT8 ? 8 : 1];
+          if (INT8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vs[i] = lds128(vc + 128 * q + 16 * i);
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int k = 32 * q + 2 * i;
@@ -659,7 +670,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
                            : make_float2(ex2_approx(x.x), ex2_approx(x.y));
             ps[i & 3] = __fadd2_rn(ps[i & 3], e);
             if (INT8) {
-              if ((i & 1) == 0) v4 = lds128(vc + 4 * k);
+              const uint4 v4 = vs[INT8 ? i / 2 : 0];
               e = __fmul2_rn(
                   e, (i & 1) ? make_float2(__uint_as_float(v4.z), __uint_as_float(v4.w))
                              : make_float2(__uint_as_float(v4.x), __uint_as_float(v4.y)));

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
         // the largest live V scale (slots past the end may hold anything)
         const float v =
             lane < G ? __uint_as_float(lds32(sa + G * 4 + 4 * (lane & (G - 1)))) : 0.0f;
-        svm = key0 + lane < g.len ? v : 0.0f;
+        svm = key0 + lane < g.len ? fabsf(v) : 0.0f;
         grow |= inv == 0.0f ? svm > 0.0f : svm * inv > 32.0f;
       }
       if (__any_sync(0xffffffffu, grow)) {
