@@ -557,8 +557,14 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
         const uint32_t kt = tile + (j >> 1);  // key tile, its scales' slot
         const uint32_t sc_at = (kt % kScRing) * kN + (j & 1) * kStep;
         const uint32_t sa = ta + (gs & 1) * kStep;
-        // INT8: the key scales, fetched before the scores they multiply are
-        // there (one by one beside them, each load's latency showed)
+        if (!wait(C::kBarS + 2 * t + (gs & 1), gs >> 1)) return ok = false;
+        tc_fence_after();
+        uint32_t sv[kStep];
+        tmem_ld32_at(sa, sv, 0);
+        tmem_ld32_at(sa, sv, 32);
+        // INT8: the key scales, all fetched while the scores arrive.  (Their
+        // barrier is waited for behind S: a warp that had no part in earlier
+        // segments could be laps ahead of it and mistake the phase.)
         uint4 ks[INT8 ? kStep / 4 : 1];
         if (INT8) {
           if (!(j & 1) && !wait(C::kBarSc + kt % kScRing, kt / kScRing))
@@ -567,11 +573,6 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kStep / 4; ++i) ks[i] = lds128(kc + 16 * i);
         }
-        if (!wait(C::kBarS + 2 * t + (gs & 1), gs >> 1)) return ok = false;
-        tc_fence_after();
-        uint32_t sv[kStep];
-        tmem_ld32_at(sa, sv, 0);
-        tmem_ld32_at(sa, sv, 32);
         tmem_ld_wait();
         if (INT8) {  // logits: the keys' scales differ
 #pragma unroll

@@ -280,6 +280,35 @@ def test_attn_paged_strided_q_scale_and_large_scores(kv, new):
     assert ((out.cpu().double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("kv", ["same", "int8"])
+def test_attn_paged_blocks_that_change_between_few_and_many_rows(kv):
+    # sequences of at most and of more than 128 packed rows by turns, long
+    # enough that every block takes several of both: the second query tile's
+    # warps sit out some of a block's segments
+    batch = 36
+    new = [3 if b % 2 else 130 for b in range(batch)]
+    lens = [1500 + 16 * b if b % 2 else 900 + b for b in range(batch)]
+    c = Cache(lens, new, 8, 64, 64, torch.float16, kv == "int8", seed=21)
+    q = torch.randn((c.cu[-1], 8, 64), generator=_gen(22)).half()
+    q[:, :, 1] *= 4
+    k, v, table, cu, ln, sc = c.device()
+    lse = torch.empty((8, c.cu[-1]), device="cuda")
+    out = tm.tilemix_attn_paged(q.cuda(), k, v, table, cu, ln, 130, max(lens),
+                                lse=lse, **sc)
+    # one head of each sequence against the oracle
+    for b in range(batch):
+        h = b % 8
+        kv1 = dict(k_scale=c.ks[:, h:h + 1], v_scale=c.vs[:, h:h + 1]) \
+            if kv == "int8" else {}
+        rows = slice(c.cu[b], c.cu[b + 1])
+        want, wl, tol = oracle.attn(q[rows, h:h + 1], c.k[:, :, h:h + 1],
+                                    c.v[:, :, h:h + 1], [c.table[b]],
+                                    [0, new[b]], [lens[b]], **kv1)
+        assert ((out[rows, h:h + 1].cpu().double() - want).abs() <= tol).all()
+        got = lse[h:h + 1, rows].cpu().double()
+        assert ((got - wl).abs() <= 2e-5 * (1 + wl.abs())).all()
+
+
 @pytest.mark.parametrize("new", [1, 64, 300])
 def test_attn_paged_bad_pages_and_lengths_keep_outputs(new):
     c = Cache([600, 600, 600, 600], [new] * 4, 1, 64, 32, torch.float16, False)
