@@ -432,8 +432,9 @@ tilemix_status tilemix_attn_prefill(const tilemix_attn_params* params,
  * Device-side checks (status word): BAD_SEQLENS for a cu_seqlens that
  * decreases or leaves [0, total_tokens], or a kv_lens entry that is negative
  * or above what the table row can hold (or max_kv_len); BAD_PAGES for a page
- * table entry in use outside [0, num_pages).  The sequences (for the append:
- * the tokens) that show the problem keep their outputs as they were.
+ * table entry in use outside [0, num_pages).  The sequences (for a bad page:
+ * the tokens, or the query rows whose keys reach it) that show the problem
+ * keep their outputs as they were.
  * ---------------------------------------------------------------------------
  */
 
@@ -563,10 +564,12 @@ typedef struct {
  * New token i of sequence b (n_b of them) goes to position kv_lens[b] - n_b
  * + i.  With freqs, K and Q are rotated exactly as tilemix_rope does and
  * rounded to dtype; INT8 pages then hold, per (token, head), a = max |x| over
- * the d channels of that 16-bit row, scale = a / 127 (IEEE fp32 division),
- * code = clamp(round_half_even(x / scale), -127, 127), scale 0 and codes 0
- * for a = 0 (the definition of tilemix_quantize_blockwise with blocks of one
- * token).  Two tokens of one call that map to the same page slot race.
+ * the d channels of that 16-bit row, scale = a * fl(1 / 127) (one fp32
+ * multiplication by the rounded reciprocal; tilemix_quantize_blockwise divides,
+ * which may differ in the last bit), code = round_half_even(x / scale) with an
+ * IEEE fp32 division, scale 0 and codes 0 for a = 0.  A row with NaN or
+ * infinity gets codes and a scale of no meaning, other rows are not affected.
+ * Two tokens of one call that map to the same page slot race.
  */
 tilemix_status tilemix_paged_append(const tilemix_append_params* params,
                                     tilemix_stream_t stream);
@@ -626,9 +629,13 @@ size_t tilemix_attn_paged_workspace_bytes(int max_q_len, int hq, int hkv,
  *   lse_i = ln sum_j exp(s_ij);  a row without a key: out 0, lse -inf
  * where INT8 pages stand for k = code * k_scale, v = code * v_scale, exactly.
  * Products run on tensor cores with fp32 accumulation; P is rounded to dtype
- * (INT8 pages: to fp16).  Slots of a page past a sequence's length may hold
- * anything, NaN included.  Results do not depend on page placement; the
- * order of summation depends on the batch's lengths, not on timing.
+ * (INT8 pages: P times the V scale to fp16, the scale relative to a power of
+ * two near the largest of its neighbours).  Slots of a page past a sequence's
+ * length may hold anything, NaN included, and so may K where the causal mask
+ * hides it; V of every position below kv_lens[b] is multiplied by a weight of
+ * 0 where it is hidden, so it has to be finite.  A NaN or +inf score makes its
+ * row NaN.  Results do not depend on page placement; the order of summation
+ * depends on the batch's lengths, not on timing.
  */
 tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* params,
                                   tilemix_stream_t stream);

@@ -45,7 +45,7 @@ def quantised(x):
     """Codes and scale of rows of the last axis, in the 32-bit arithmetic
     that defines them."""
     a = x.float().abs().amax(-1)
-    scale = a / 127.0
+    scale = a * (torch.ones(()) / 127.0)
     safe = torch.where(scale > 0, scale, torch.ones_like(scale))
     q = (x.float() / safe[..., None]).round().clamp(-127, 127).to(torch.int8)
     return q, scale

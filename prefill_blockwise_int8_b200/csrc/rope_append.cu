@@ -5,9 +5,10 @@
 // x_b) -> (x_a c - x_b s, x_b c + x_a s).  The angle is formed in double, p
 // f_i / 2 pi is reduced to [-1/2, 1/2] turns there, and only the remainder
 // becomes fp32, so the rotation of position 10^6 is as exact as that of 10.
-// INT8 rows take absmax / 127 over their d channels (of the row as rounded to
-// 16 bits, so that append(x) after a rotary call and the fused append agree
-// bit for bit) and the quantiser's code definition (quant_code.cuh).
+// INT8 rows take absmax times fl(1 / 127) over their d channels (of the row as
+// rounded to 16 bits, so that append(x) after a rotary call and the fused
+// append agree bit for bit) and the quantiser's code definition for that scale
+// (quant_code.cuh; |x / scale| stays below 127.0001).
 //
 // What bounds it: memory traffic.  One block takes a few tokens: its threads
 // first make the tokens' cosines and sines (shared by all heads) in shared
@@ -26,6 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;  // of a block
 constexpr double kInvTwoPi = 0.15915494309189533577;
+constexpr float kInv127 = 1.0f / 127.0f;
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int o = units >> 1; o > 0; o >>= 1)
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (live && !is_q) {
-          const float sc = __fdiv_rn(m, 127.0f);
+          const float sc = __fmul_rn(m, kInv127);
           const float rcp = m != 0.0f ? __frcp_rn(sc) : 0.0f;
           uint32_t ca[8], cb[8];
           quant_codes8(fa, sc, rcp, ca);
