@@ -551,6 +551,8 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       // keys that every live row of the warp's tile sees
       const int lim_min = keys_of_token(p, s.g, s.tok0 + t * kM / p.group);
       float m_run = -CUDART_INF_F, l_run = 0.0f;
+      // INT8: sums of the weights P sv 2^-E as O has them, rounded, and before
+      float l_rnd = 0.0f, l_wgt = 0.0f;
       float inv = 0.0f;
       for (int j = 0; j < s.steps; ++j, ++gs) {
         const int key0 = s.ua * kN + j * kStep;
@@ -633,6 +635,10 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
           if (!wait(C::kBarO + 2 * t + ((gs - 1) & 1), (gs - 1) >> 1))
             return ok = false;
           tc_fence_after();
+          if (INT8) {
+            l_rnd *= alpha;
+            l_wgt *= alpha;
+          }
 #pragma unroll 1
           for (int oc = 0; oc < D; oc += 64) {
             uint32_t o[64];
@@ -646,11 +652,20 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
             for (int i = 0; i < 64; i += 16) tmem_st16(ta + 128 + oc + i, o + i);
           }
         }
+        // INT8: P sv is never exact, not even of the key that dominates a
+        // row, so its rounding is followed and divided out at the end (see
+        // round_off); where no key has 1/32 of its row so far the roundings
+        // average out.  (Ragged chunks 524 us without it, 576 with it, 596
+        // with it in every step.  16-bit P of a row's maximum is exact unless
+        // the reference lags, and following it took 1.05 times as long.)
+        const bool heavy =
+            INT8 && __any_sync(0xffffffffu,
+                               !(ex2_approx(mx - m_run) < 0.03125f * l_run));
         const float mu = m_run == -CUDART_INF_F ? 0.0f : m_run;
         const float2 c2 = make_float2(c, c), nm = make_float2(-mu, -mu);
-        float2 ps[4];
+        float2 ps[2], pr[2], pw[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ps[k] = make_float2(0.f, 0.f);
+        for (int k = 0; k < 2; ++k) ps[k] = pr[k] = pw[k] = make_float2(0.f, 0.f);
         const uint32_t vc = smem_u32(vsc + sc_at);
 #pragma unroll
         for (int q = 0; q < kStep / 32; ++q) {
@@ -669,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
             float2 e = (i & 7) < C::kPolyOf8
                            ? ex2_poly2(x)
                            : make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            ps[i & 3] = __fadd2_rn(ps[i & 3], e);
+            ps[i & 1] = __fadd2_rn(ps[i & 1], e);
             if (INT8) {
               const uint4 v4 = vs[INT8 ? i / 2 : 0];
               e = __fmul2_rn(
@@ -677,12 +692,25 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
                              : make_float2(__uint_as_float(v4.x), __uint_as_float(v4.y)));
             }
             pk[i] = pack_pair<BF16 && !INT8>(e.x, e.y);
+            if (INT8) pw[i & 1] = __fadd2_rn(pw[i & 1], e);
+          }
+          if (INT8 && heavy) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pr[i & 1] = __fadd2_rn(pr[i & 1], unpack_pair<BF16 && !INT8>(pk[i]));
           }
           tmem_st16(sa + 16 * q, pk);
         }
-        const float2 s2 =
-            __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
-        l_run += s2.x + s2.y;
+        auto total = [](const float2(&x)[2]) {
+          const float2 y = __fadd2_rn(x[0], x[1]);
+          return y.x + y.y;
+        };
+        l_run += total(ps);
+        if (INT8) {
+          const float wgt = total(pw);
+          l_wgt += wgt;
+          l_rnd += heavy ? total(pr) : wgt;
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -698,7 +726,8 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       const bool live = row < s.nrows && !(whole && bad);
       const int tok = s.g.start + s.tok0 + row / p.group;
       const int h = s.head0 + row % p.group;
-      float f = INT8 ? (inv > 0.0f ? 1.0f / inv : 0.0f) : 1.0f;
+      float f = 1.0f;  // O of the exact weights, at the scale of V
+      if (INT8) f = inv > 0.0f ? round_off(l_wgt, l_rnd) / inv : 0.0f;
       if (whole) f = l_run == 0.0f ? 0.0f : f / l_run;
       const bool none = whole && l_run == 0.0f;
       uint16_t* dst = p.out + (static_cast<int64_t>(tok) * p.hq + h) * D;

@@ -254,6 +254,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
       for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F};  // running max (base 2)
     float l[2] = {0.0f, 0.0f};                    // this thread's sums
+    // sums of the weights as O has them: rounded, and (INT8: with their
+    // scales) before that
+    float lr[2] = {0.0f, 0.0f}, lw[2] = {0.0f, 0.0f};
     float inv = 0.0f;  // INT8: 2^-E of the V scales (0: none seen)
 
     for (int i = 0; i < nst; ++i) {
@@ -374,6 +377,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
           }
           l[r] *= al[r];
           al[r] *= f;
+          lr[r] *= al[r];
+          lw[r] *= al[r];
         }
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
@@ -409,8 +414,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
             l[e >> 1] += e4[e];
             if (INT8) e4[e] *= (e & 1) ? vb_ : va_;
           }
-          pf[2 * jj] = pack_pair<BF16 && !INT8>(e4[0], e4[1]);
-          pf[2 * jj + 1] = pack_pair<BF16 && !INT8>(e4[2], e4[3]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            pf[2 * jj + r] = pack_pair<BF16 && !INT8>(e4[2 * r], e4[2 * r + 1]);
+            const float2 x = unpack_pair<BF16 && !INT8>(pf[2 * jj + r]);
+            lr[r] += x.x + x.y;
+            if (INT8) lw[r] += e4[2 * r] + e4[2 * r + 1];
+          }
         }
         if (INT8) {
           // any int8 code is finite: P = 0 is enough behind the end.
@@ -488,28 +498,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
 
     // ---- the four warps' results merge through their own rings ----
     float* mine = reinterpret_cast<float*>(ring);
-    if (INT8) {  // back to the scale of V
-      const float e = inv > 0.0f ? 1.0f / inv : 0.0f;
+    float back[2];  // O of the exact weights, INT8: back to the scale of V
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[j][k] *= e;
+    for (int r = 0; r < 2; ++r) {
+      auto quad = [](float x) {
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        return x + __shfl_xor_sync(0xffffffffu, x, 2);
+      };
+      l[r] = quad(l[r]);
+      back[r] = round_off(INT8 ? quad(lw[r]) : l[r], quad(lr[r]));
+      if (INT8) back[r] = inv > 0.0f ? back[r] / inv : 0.0f;
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       float* row = mine + (g8 + 8 * r) * C::kMergeStride;
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         if (INT8) {
           // tiles 2 j', 2 j' + 1: channels 16 j' + 4 q4 + {0, 2} and {1, 3}
           const int c = 16 * (j >> 1) + 4 * q4 + (j & 1);
-          row[c] = o[j][2 * r];
-          row[c + 2] = o[j][2 * r + 1];
+          row[c] = o[j][2 * r] * back[r];
+          row[c + 2] = o[j][2 * r + 1] * back[r];
         } else {
           *reinterpret_cast<float2*>(row + 8 * j + 2 * q4) =
-              make_float2(o[j][2 * r], o[j][2 * r + 1]);
+              make_float2(o[j][2 * r] * back[r], o[j][2 * r + 1] * back[r]);
         }
       }
       if (q4 == 0) {

@@ -252,6 +252,22 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   return pack_half2(lo, hi);
 }
 
+// The two 16-bit values of a packed pair, exactly.
+template <bool BF16>
+__device__ __forceinline__ float2 unpack_pair(uint32_t w) {
+  if (BF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Sum of the weights over the sum of what their rounding to 16 bits left:
+// O of the rounded weights times it is a mean of V again.  Without it a row
+// that one key dominates is off by that key's rounding (1.4 times the error
+// of rounding the output alone).
+__device__ __forceinline__ float round_off(float sum, float rounded) {
+  return rounded != 0.0f ? sum / rounded : 1.0f;
+}
+
 // ln of 2^m l; -inf where nothing was summed.
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l != 0.0f ? (m + log2f(l)) * 0.69314718055994530942f : -CUDART_INF_F;
