@@ -281,6 +281,56 @@ def test_attn_paged_strided_q_scale_and_large_scores(kv, new):
 
 
 @pytest.mark.parametrize("kv", ["same", "int8"])
+@pytest.mark.parametrize("new", [5, 200])
+def test_attn_paged_non_finite_keys_reach_their_rows_only(new, kv):
+    # key 400 + new - 3 is seen by the last three rows; a NaN there makes them
+    # NaN, an infinity too (by the formula: inf - inf), the others stay
+    c = Cache([400 + new, 300 + new], [new, new], 2, 64, 32, torch.float16,
+              kv == "int8", seed=31)
+    q = torch.rand((2 * new, 4, 64), generator=_gen(32)).half() + 0.1
+    at = 400 + new - 3
+    pid, slot = int(c.table[0, at // 32]), at % 32
+    for bad in (math.nan, math.inf):
+        k, v, table, cu, lens, sc = c.device()
+        if kv == "int8":
+            k[pid, slot] = 1  # scores of one sign
+            sc["k_scale"][pid, :, slot] = bad
+        else:
+            k[pid, slot, :, 7] = bad
+        want, wl, tol = oracle.attn(q, c.k, c.v, c.table, c.cu, c.lens,
+                                    k_scale=c.ks, v_scale=c.vs)
+        lse = torch.empty((4, 2 * new), device="cuda")
+        out = tm.tilemix_attn_paged(q.cuda(), k, v, table, cu, lens, new,
+                                    400 + new, lse=lse, **sc).cpu().double()
+        hit = torch.zeros(2 * new, dtype=torch.bool)
+        hit[new - 3:new] = True
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse.cpu()[:, hit]).all()
+        assert ((out[~hit] - want[~hit]).abs() <= tol[~hit]).all()
+        assert torch.isfinite(lse.cpu()[:, ~hit]).all()
+
+
+@pytest.mark.parametrize("new", [1, 9])
+def test_append_and_attn_paged_many_sequences(new):
+    # far more sequences than a warp looks at in one step
+    batch, hq, hkv, d, page = 1100, 4, 1, 64, 16
+    g = _gen(41)
+    lens = (torch.randint(0, 40, (batch,), generator=g) + new).tolist()
+    c = Cache(lens, [new] * batch, hkv, d, page, torch.bfloat16, False, seed=42)
+    x = torch.randn((batch * new, hq + 2 * hkv, d), generator=g).bfloat16()
+    k, v, table, cu, ln, _ = c.device()
+    dev = x.cuda()
+    tm.tilemix_paged_append(dev[:, hq:hq + 1], dev[:, hq + 1:], table, cu, ln, k, v)
+    for t, b, p, pid, slot in oracle.places(c.cu, lens, c.table.tolist(), page):
+        c.k[pid, slot], c.v[pid, slot] = x[t, hq:hq + 1], x[t, hq + 1:]
+    live = c.live
+    assert torch.equal(k.cpu()[live], c.k[live])
+    assert torch.equal(v.cpu()[live], c.v[live])
+    out = tm.tilemix_attn_paged(dev[:, :hq], k, v, table, cu, ln, new, max(lens))
+    want, _, tol = oracle.attn(x[:, :hq], c.k, c.v, c.table, c.cu, lens)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
 def test_attn_paged_blocks_that_change_between_few_and_many_rows(kv):
     # sequences of at most and of more than 128 packed rows by turns, long
     # enough that every block takes several of both: the second query tile's
@@ -379,10 +429,10 @@ def test_attn_paged_graph_replays_with_new_lengths(new):
     assert torch.equal(out, want)      # same lengths, same order of sums
 
 
-def test_attn_paged_two_streams_at_once_and_repeatable():
-    new = 1
+@pytest.mark.parametrize("new", [1, 150])
+def test_attn_paged_two_streams_at_once_and_repeatable(new):
     c = Cache([900, 3000], [new, new], 2, 128, 64, torch.float16, True, seed=4)
-    q = torch.randn((2, 16, 128), generator=_gen(5)).half()
+    q = torch.randn((2 * new, 16, 128), generator=_gen(5)).half()
     d = c.device()
     want, wl = _check_attn(c, q, True, device=d)
     k, v, table, cu, lens, kw = d
@@ -392,7 +442,7 @@ def test_attn_paged_two_streams_at_once_and_repeatable():
     outs = []
     for _ in range(5):
         for s in streams:
-            outs.append(tm.tilemix_attn_paged(qd, k, v, table, cu, lens, 1,
+            outs.append(tm.tilemix_attn_paged(qd, k, v, table, cu, lens, new,
                                               3000, stream=s, **kw))
     torch.cuda.synchronize()
     for o in outs:
