@@ -1,6 +1,6 @@
-// Attention of few new tokens over a paged KV cache (decoded tokens, drafted
-// ones; any other call too, at the cost of reading the cache once per 16
-// packed rows).
+// Attention of few new tokens over a paged KV cache: calls of at most 16 packed
+// rows a sequence (decoded tokens).  It would serve any call, at the cost of
+// reading the cache once per 16 rows.
 //
 // Mathematics.  The query heads of one KV head and the new tokens pack into
 // rows (row = token * group + head), so a KV head's keys are read once for
@@ -23,11 +23,14 @@
 // another, and the split follows from the lengths alone.
 //
 // What bounds it: HBM.  Each warp owns every fourth group of 16 or 32 keys of
-// a block's part and runs alone (private m, l, O and a private ring of TMA slots, no
-// block barrier in the loop), so a block keeps 4 rings of loads in flight.
-// The products are small (two m16n8k16 per key for d = 128, a fifth of the
-// tensor rate at full HBM speed), hence warp-level mma fragments that never
-// leave registers.
+// a block's part and runs alone (private m, l, O and a private ring of TMA
+// slots, no block barrier in the loop), so a block keeps 4 rings of loads in
+// flight.  The products are small (two m16n8k16 per key for d = 128, a fifth
+// of the tensor rate at full HBM speed), hence warp-level mma fragments that
+// never leave registers.  64 single tokens over 1K..32K keys, 32/8 heads, d
+// 128: 705 us, 6.3 TB/s.  INT8 keys are bound by instructions instead (code
+// conversion and its latencies): 8 tokens over 8K..16K, 32/32 heads, 176 us,
+// 4.6 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
