@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  pdl_wait();
   clear_headers(p);
   pdl_launch();
   tc_fence_before();
@@ -801,8 +802,7 @@ cudaError_t launch_one(const PagedArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<kGridMax, C::kThreads, C::kSmem, stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_behind(kern, dim3(kGridMax), dim3(C::kThreads), C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   const int rows = static_cast<int>(
       min(static_cast<long long>(kRows),

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
     tma_prefetch_desc(&p.tm_v);
   }
   if (threadIdx.x == 0) s_bad = 0;
+  pdl_wait();
   clear_headers(p);
   pdl_launch();
   const Line<kRows, C::kUnit> line(p);
@@ -617,8 +618,7 @@ cudaError_t launch_one(PagedArgs a, cudaStream_t stream) {
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   constexpr int grid = 148 * kBlocksPerSm<D, INT8>;
-  kern<<<grid, kThreads, C::kSmem, stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_behind(kern, dim3(grid), dim3(kThreads), C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   const int rows = static_cast<int>(
       min(static_cast<long long>(kRows),

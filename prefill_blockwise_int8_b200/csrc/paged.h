@@ -82,6 +82,24 @@ constexpr int paged_step_group(int head_dim, bool int8) {
   return head_dim == 128 && !int8 ? 16 : 32;
 }
 
+// Launches a kernel that may be scheduled while the one before it on the
+// stream drains; it has to wait (pdl_wait) before it touches memory.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The step kernel (up to 16 packed rows a pass) and the chunk kernel (256);
 // each has its own workspace size.
 size_t paged_step_workspace_bytes(int head_dim);

@@ -235,14 +235,6 @@ __device__ __forceinline__ void clear_headers(const PagedArgs& p) {
     p.head[2 * (2 * blockIdx.x + threadIdx.x)] = make_int4(0, 0, 0, 0);
 }
 
-__device__ __forceinline__ void pdl_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-__device__ __forceinline__ void pdl_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   if (BF16) {
@@ -416,17 +408,9 @@ __global__ void __launch_bounds__(32 * W * ROWS)
 template <int D, bool BF16, int R, int W, int ROWS>
 cudaError_t launch_merge(const PagedArgs& a, int blocks, int rows,
                          cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, (rows + ROWS - 1) / ROWS);
-  cfg.blockDim = dim3(32 * W * ROWS);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, BF16, R, W, ROWS>, a,
-                            blocks);
+  return launch_behind(paged_merge_kernel<D, BF16, R, W, ROWS>,
+                       dim3(blocks, (rows + ROWS - 1) / ROWS), dim3(32 * W * ROWS),
+                       0, stream, a, blocks);
 }
 
 // Workspace: headers first, then the partial rows.

@@ -22,6 +22,7 @@
 
 #include "internal.h"
 #include "paged.h"
+#include "ptx.cuh"
 #include "quant_code.cuh"
 
 namespace tilemix {
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kThreads)
     rope_kernel(const __grid_constant__ RopeArgs p, int tokens_per_block) {
   extern __shared__ float2 cs_all[];  // [tokens_per_block][rot_dim / 2]
   __shared__ Place place[kMaxTokens];
+  pdl_wait();
   const int t0 = blockIdx.x * tokens_per_block;
   const int nt = min(tokens_per_block, p.total_tokens - t0);
   const int half = p.rot_dim >> 1;
@@ -323,8 +325,8 @@ cudaError_t launch_one(const RopeArgs& a, cudaStream_t stream) {
   const int tpb = a.total_tokens >= 1024 ? kMany : 1;
   const int grid = (a.total_tokens + tpb - 1) / tpb;
   const size_t smem = a.freqs ? tpb * (a.rot_dim / 2) * sizeof(float2) : 0;
-  rope_kernel<BF16, MODE><<<grid, kThreads, smem, stream>>>(a, tpb);
-  return cudaGetLastError();
+  return launch_behind(rope_kernel<BF16, MODE>, dim3(grid), dim3(kThreads), smem,
+                       stream, a, tpb);
 }
 
 }  // namespace
