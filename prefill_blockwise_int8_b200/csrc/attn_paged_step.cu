@@ -1,6 +1,6 @@
 // Attention of few new tokens over a paged KV cache: calls of at most 16 packed
-// rows a sequence (decoded tokens).  It would serve any call, at the cost of
-// reading the cache once per 16 rows.
+// rows a sequence (INT8: 32), as decoded tokens are.  It would serve any call,
+// at the cost of reading the cache once per 16 rows.
 //
 // Mathematics.  The query heads of one KV head and the new tokens pack into
 // rows (row = token * group + head), so a KV head's keys are read once for

@@ -100,8 +100,8 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The step kernel (up to 16 packed rows a pass) and the chunk kernel (256);
-// each has its own workspace size.
+// The step kernel (16 packed rows a pass) and the chunk kernel (256); each has
+// its own workspace size.
 size_t paged_step_workspace_bytes(int head_dim);
 size_t paged_chunk_workspace_bytes(int head_dim);
 

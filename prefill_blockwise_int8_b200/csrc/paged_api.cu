@@ -98,9 +98,12 @@ tilemix_status check_heads(const char* where, int hq, int hkv) {
 }
 
 // Which attention kernel: the step kernel reads the cache once per 16 packed
-// rows, the chunk kernel once per 256.
-bool use_step(int max_q_len, int group) {
-  return static_cast<long long>(max_q_len) * group <= 16;
+// rows, the chunk kernel once per 256 but with more to begin and end.  16
+// sequences of 6000 keys, d 128, step against chunk: 16 rows 50 / 49 us, 24
+// rows 75 / 49; 4000 keys of one sequence 8 rows 19 / 21.  INT8, whose chunk
+// kernel converts tiles first: 16 rows 49 / 88, 32 rows 71 / 89.
+bool use_step(int max_q_len, int group, bool int8) {
+  return static_cast<long long>(max_q_len) * group <= (int8 ? 32 : 16);
 }
 
 // {d, page_size, hkv, num_pages} map over a page array.
@@ -356,7 +359,8 @@ size_t tilemix_attn_paged_workspace_bytes(int max_q_len, int hq, int hkv,
   if (max_q_len < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq / hkv > 128 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return use_step(max_q_len, hq / hkv)
+  // (of 17 to 32 rows either kernel may come: the chunk kernel needs more)
+  return use_step(max_q_len, hq / hkv, false)
              ? tilemix::paged_step_workspace_bytes(head_dim)
              : tilemix::paged_chunk_workspace_bytes(head_dim);
 }
@@ -412,7 +416,7 @@ tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
   memset(&p, 0, sizeof(p));
   const CUtensorMapSwizzle sw = int8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                 : CU_TENSOR_MAP_SWIZZLE_128B;
-  const bool step = use_step(a->max_q_len, a->hq / a->hkv);
+  const bool step = use_step(a->max_q_len, a->hq / a->hkv, int8);
   const int most = step ? tilemix::paged_step_group(d, int8) : 128;
   const int box = a->page_size < most ? a->page_size : most;
   if (!make_pages_map(&p.tm_k, a->k_pages, int8, bf16, d, a->page_size, a->hkv,

@@ -190,6 +190,9 @@ def test_attn_refuses(over, expect):
 def test_workspace_bytes():
     ws = tm.tilemix_attn_paged_workspace_bytes
     assert 0 < ws(1, 32, 8, 64) < ws(1, 32, 8, 128) < 64 << 20
+    # it grows with max_q_len at most, so one for the longest call serves all
+    sizes = [ws(n, 28, 4, 128) for n in (0, 1, 2, 3, 4, 5, 40, 5000)]
+    assert sizes == sorted(sizes)
     for bad in ((-1, 32, 8, 128), (1, 0, 8, 128), (1, 32, 0, 128),
                 (1, 30, 8, 128), (1, 32, 8, 96), (1, 129, 1, 128)):
         assert ws(*bad) == 0

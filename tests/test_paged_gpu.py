@@ -232,6 +232,9 @@ SHAPES = [
     ([257, 300], [700, 300], 4, 4, 128, 16),
     ([300, 7, 140], [1024, 500, 141], 8, 1, 128, 128),
     ([513], [1500], 3, 1, 64, 32),
+    ([3, 0, 2], [100, 33, 700], 16, 2, 128, 16),   # 17 to 32 packed rows
+    ([1, 1], [90, 2500], 24, 1, 64, 32),           # a group above 16
+    ([4], [1000], 32, 4, 64, 16),
 ]
 
 
