@@ -7,7 +7,8 @@
 // codes convert exactly to the query's type and their scale multiplies the
 // fp32 score; V codes convert exactly to fp16 and their scale joins P as P sv
 // 2^-E, 2^E a power of two near the scales seen (raised, with O rescaled, when
-// a scale passes 16 times it), so that products stay inside fp16's range.
+// a scale passes 16 times it), so that products stay inside fp16's range.  The
+// sign of a V scale goes to its codes, so weights are never negative.
 //
 // B200 design.  One CTA per SM takes an equal part of the line of all items
 // (256 packed rows of a sequence and KV head, times its keys in units of
@@ -147,10 +148,11 @@ __device__ __forceinline__ void for_segments(const PagedArgs& p,
 }
 
 // One key row of codes (D bytes at row r of `src`, swizzled) -> 16-bit row r
-// of a K or V tile (D/64 chunks of [128][128 B], 128-byte swizzle).
-template <int D, bool BF16>
+// of a K or V tile (D/64 chunks of [128][128 B], 128-byte swizzle).  FLIP:
+// the signs of all of them are changed where `flip` is the pair's sign bits.
+template <int D, bool BF16, bool FLIP = false>
 __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst,
-                                              int r) {
+                                              int r, uint32_t flip = 0) {
   constexpr uint32_t sm = D == 128 ? 7u : 3u;
 #pragma unroll
   for (int u = 0; u < D / 16; ++u) {
@@ -161,6 +163,7 @@ __device__ __forceinline__ void convert_codes(const uint8_t* src, uint8_t* dst,
     for (int i = 0; i < 4; ++i) {
       if (BF16) i8x4_to_bf2x2(w[i], h[2 * i], h[2 * i + 1]);
       else i8x4_to_h2x2(w[i], h[2 * i], h[2 * i + 1]);
+      if (FLIP) h[2 * i] ^= flip, h[2 * i + 1] ^= flip;
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -462,6 +465,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       for_segments(p, line, begin, end, [&](const Segment& s, int) {
         inv = 0.0f;  // O begins anew with every segment
         for (int n = s.ua; n < s.ub; ++n, ++tile) {
+          uint32_t flip = 0;  // sign bits of a pair, where this row's V scale is < 0
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++idx) {
             const uint32_t raw = idx % (INT8 ? C::kRawSlots : 1);
@@ -491,14 +495,19 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
                 inv = ldexpf(1.0f, -e);
               }
               ksc[sr * kN + r] = r < live ? sc[r] * p.scale_log2 : 0.0f;
-              vsc[sr * kN + r] = r < live ? sv[r] * inv : 0.0f;
+              // weights keep one sign (see round_off); V's codes take it
+              vsc[sr * kN + r] = r < live ? fabsf(sv[r]) * inv : 0.0f;
+              flip = sv[r] < 0.0f ? 0x80008000u : 0u;
               if (r == 0) vexp[sr] = inv;
               __syncwarp();
               if (lane == 0) mbar_arrive(&bars[C::kBarSc + sr]);
               convert_codes<D, BF16>(src, dst, r);
             } else {
               // rows behind the end: any code is finite, and P is 0 there
-              convert_codes<D, false>(src, dst, r);
+              if (__any_sync(0xffffffffu, flip != 0))
+                convert_codes<D, false, true>(src, dst, r, flip);
+              else
+                convert_codes<D, false>(src, dst, r);
             }
             fence_proxy_async_smem();
             __syncwarp();

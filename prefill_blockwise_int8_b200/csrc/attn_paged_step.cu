@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
       for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F};  // running max (base 2)
     float l[2] = {0.0f, 0.0f};                    // this thread's sums
-    // sums of the weights as O has them: rounded, and (INT8: with their
-    // scales) before that
+    // sums of the weights as O has them: rounded, and (INT8: times the size
+    // of their scales) before that
     float lr[2] = {0.0f, 0.0f}, lw[2] = {0.0f, 0.0f};
     float inv = 0.0f;  // INT8: 2^-E of the V scales (0: none seen)
 
@@ -422,8 +422,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
           for (int r = 0; r < 2; ++r) {
             pf[2 * jj + r] = pack_pair<BF16 && !INT8>(e4[2 * r], e4[2 * r + 1]);
             const float2 x = unpack_pair<BF16 && !INT8>(pf[2 * jj + r]);
-            lr[r] += x.x + x.y;
-            if (INT8) lw[r] += e4[2 * r] + e4[2 * r + 1];
+            // (sizes: weights of both signs would cancel in the ratio)
+            lr[r] += fabsf(x.x) + fabsf(x.y);
+            if (INT8) lw[r] += fabsf(e4[2 * r]) + fabsf(e4[2 * r + 1]);
           }
         }
         if (INT8) {

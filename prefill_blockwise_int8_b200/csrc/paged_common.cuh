@@ -71,10 +71,11 @@ __device__ __forceinline__ float2 unpack_pair(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// Sum of the weights over the sum of what their rounding to 16 bits left:
-// O of the rounded weights times it is a mean of V again.  Without it a row
-// that one key dominates is off by that key's rounding (1.4 times the error
-// of rounding the output alone).
+// Sum of the weights' sizes over the sum of what their rounding to 16 bits
+// left: O of the rounded weights times it is a mean of V again.  Without it a
+// row that one key dominates is off by that key's rounding (1.4 times the
+// error of rounding the output alone).  Sizes, since INT8 scales may have
+// either sign: every term is off by at most a half step, so the ratio is too.
 __device__ __forceinline__ float round_off(float sum, float rounded) {
   return rounded != 0.0f ? sum / rounded : 1.0f;
 }

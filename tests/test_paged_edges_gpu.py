@@ -46,3 +46,53 @@ def test_attn_paged_nobody_active(most):
     tm.tilemix_attn_paged(q, k, v, table, cu, lens, most, 2000, out=out,
                           status=status)
     assert int(status.item()) == 0 and (out == 7).all()
+
+
+# ---------------------------------------------------------------------------
+# V scales of any size and sign (an INT8 value is code * scale, exactly)
+# ---------------------------------------------------------------------------
+
+def _v_scales(kind, shape, pos, gen):
+    """Scales [keys, heads] of one sequence's keys at positions pos."""
+    x = torch.rand(shape, generator=gen) + 0.5
+    sign = torch.where(torch.rand(shape, generator=gen) < 0.5, -1.0, 1.0)
+    if kind == "mixed":
+        return x * sign
+    if kind == "cancel":   # signed sums of weights nearly vanish
+        return 0.7 * (1 + 1e-5 * x) * torch.where(pos % 2 == 0, 1.0, -1.0)[:, None]
+    if kind == "negative":
+        return -x
+    if kind == "rising":   # the reference is raised again and again
+        return x * sign * 2.0 ** (pos[:, None] / 16.0 - 44)
+    if kind == "falling":  # tiny beside the first
+        return x * 2.0 ** (6 - pos[:, None] / 40.0)
+    # nothing but zeros, then some
+    return torch.where((pos // 100 % 2 == 0)[:, None], torch.zeros(()), x * sign)
+
+
+@pytest.mark.parametrize("kind", ["mixed", "cancel", "negative", "rising",
+                                  "falling", "zeros"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("new,d", [(1, 128), (5, 64), (40, 128), (200, 64)])
+def test_attn_paged_v_scales_of_any_size_and_sign(new, d, dtype, kind):
+    # one token and 20 rows: step kernel; more: chunk kernel
+    c = Cache([700, 301], [new, new], 2, d, 32, dtype, True, seed=new)
+    g = _gen(71)
+    for b, n in enumerate(c.lens):
+        pos = torch.arange(n)
+        ids = c.table[b].long()[pos // 32]
+        c.vs[ids, :, pos % 32] = _v_scales(kind, (n, 2), pos, g)
+    if kind == "cancel":
+        c.k.zero_()        # all keys weigh the same
+    q = torch.randn((2 * new, 8, d), generator=_gen(72)).to(dtype)
+    k, v, table, cu, lens, sc = c.device()
+    out = tm.tilemix_attn_paged(q.cuda(), k, v, table, cu, lens, new, 700, **sc)
+    args = (c.table, c.cu, c.lens)
+    want, _, tol = oracle.attn(q, c.k, c.v, *args, k_scale=c.ks, v_scale=c.vs)
+    # weights are rounded to fp16, and O is multiplied by the ratio of their
+    # sums before and after: each off by at most 2^-11 of sum_j p_j |v_j|, of
+    # which `tol` counts the first
+    size, _, _ = oracle.attn(q, c.k, c.v.short().abs(), *args, k_scale=c.ks,
+                             v_scale=c.vs.abs())
+    err = (out.cpu().double() - want).abs()
+    assert (err <= tol + 2.0 ** -11 * size).all(), (err / (tol + 2.0 ** -11 * size)).max()
