@@ -99,7 +99,8 @@ struct Cfg {
   static constexpr int kBarRawFull = kBarEmpty + kSlots;
   static constexpr int kBarRawEmpty = kBarRawFull + kRawSlots;
   static constexpr int kBarSc = kBarRawEmpty + kRawSlots;  // [kScRing]
-  static constexpr int kBarDrain = kBarSc + (INT8 ? kScRing : 0);
+  static constexpr int kBarBad = kBarSc + (INT8 ? kScRing : 0);  // [kBadRing]
+  static constexpr int kBarDrain = kBarBad + kBadRing;
   static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kSmem = kBarOff + 8 * kNumBars + 16 + 1024;
   static_assert(kSmem + 64 <= 232448, "shared memory");
@@ -216,6 +217,8 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
         mbar_init(&bars[C::kBarSc + s], 4);
       }
     }
+    for (int s = 0; s < kBadRing; ++s)
+      mbar_init(&bars[C::kBarBad + s], 8);  // one arrival per softmax warp
     mbar_init(&bars[C::kBarDrain], 1);
     mbar_init(&bars[C::kBarDrain + 1], 1);
     *abort_flag = 0;
@@ -268,6 +271,14 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       uint32_t idx = 0;  // tiles loaded
       bool ok = true;
       for_segments(p, line, begin, end, [&](const Segment& s, int b) {
+        // The entry is free once every softmax warp has read it.  (Segments of
+        // one query tile leave the other tile's warps behind; only this keeps
+        // their lead within the ring.)
+        if (s.index >= kBadRing &&
+            !wait(C::kBarBad + s.index % kBadRing, s.index / kBadRing - 1)) {
+          ok = false;
+          return false;
+        }
         if (lane == 0) bad_ring[s.index % kBadRing] = 0;
         __syncwarp();
         const int32_t* trow = p.page_table + b * p.table_stride;
@@ -535,6 +546,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
     for_segments(p, line, begin, end, [&](const Segment& s, int) {
       if (t * kM >= s.nrows) {
         tile += s.ub - s.ua;
+        if (lane == 0) mbar_arrive(&bars[C::kBarBad + s.index % kBadRing]);
         return true;
       }
       // ---- Q: D/8 threads a row, 16 bytes each ----
@@ -739,6 +751,8 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       tc_fence_after();
       const bool whole = s.ua == 0 && s.ub == s.units;
       const bool bad = bad_ring[s.index % kBadRing] != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[C::kBarBad + s.index % kBadRing]);
       const int slot = 2 * blockIdx.x + (s.ua == 0 ? 1 : 0);
       const bool live = row < s.nrows && !(whole && bad);
       const int tok = s.g.start + s.tok0 + row / p.group;

@@ -96,3 +96,35 @@ def test_attn_paged_v_scales_of_any_size_and_sign(new, d, dtype, kind):
                              v_scale=c.vs.abs())
     err = (out.cpu().double() - want).abs()
     assert (err <= tol + 2.0 ** -11 * size).all(), (err / (tol + 2.0 ** -11 * size)).max()
+
+
+# ---------------------------------------------------------------------------
+# bad pages
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+def test_attn_paged_bad_pages_before_many_short_segments(kv):
+    # every 12th sequence fills both query tiles of a block and shows a bad
+    # page; the short ones behind it, 8 and more in the same block, use one
+    # tile only and run ahead of the other
+    batch = 1900
+    new = [200 if b % 12 == 0 else 20 for b in range(batch)]
+    c = Cache([n + 16 for n in new], new, 1, 64, 32, torch.float16,
+              kv == "int8", seed=81)
+    q = torch.randn((c.cu[-1], 1, 64), generator=_gen(82)).half().cuda()
+    k, v, table, cu, lens, sc = c.device()
+    call = lambda t, **kw: tm.tilemix_attn_paged(q, k, v, t, cu, lens, 200, 216,
+                                                 **sc, **kw)
+    good = call(table)
+    broken = table.clone()
+    broken[::12, 0] = 1 << 20
+    out = torch.full_like(good, 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call(broken, out=out, status=status)
+    assert int(status.item()) == BAD_PAGES
+    hit = torch.zeros(c.cu[-1], dtype=torch.bool)
+    for b in range(0, batch, 12):
+        hit[c.cu[b]:c.cu[b + 1]] = True
+    hit = hit.cuda()
+    assert torch.equal(out[~hit], good[~hit]) and torch.isfinite(good).all()
+    assert (out[hit] == 7).all()
