@@ -434,7 +434,7 @@ tilemix_status tilemix_attn_prefill(const tilemix_attn_params* params,
  * or above what the table row can hold (or max_kv_len); BAD_PAGES for a page
  * table entry in use outside [0, num_pages).  The sequences (for a bad page:
  * the tokens, or the query rows whose keys reach it) that show the problem
- * keep their outputs as they were.
+ * keep their outputs as they were; the others are computed.
  * ---------------------------------------------------------------------------
  */
 

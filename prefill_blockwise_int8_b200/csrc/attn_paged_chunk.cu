@@ -51,7 +51,6 @@ constexpr int kStep = 64;     // keys of a softmax step
 constexpr int kGridMax = 148;
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpConv = 12;
 constexpr int kScRing = 4;    // tiles whose INT8 scales are kept
-constexpr int kBadRing = 8;   // segments whose page check is kept
 
 template <int D, bool BF16, bool INT8>
 struct Cfg {
@@ -84,11 +83,12 @@ struct Cfg {
   static constexpr int kRingOff = 2 * kQTile;
   static constexpr int kRawOff = kRingOff + kSlots * kTile;
   static constexpr int kRawScOff = kRawOff + kRawSlots * kRaw;  // [raw][2][128]
-  static constexpr int kKscOff = kRawScOff + kRawSlots * kN * 8;
+  static constexpr int kRawLiveOff = kRawScOff + kRawSlots * kN * 8;  // [raw] ints
+  static constexpr int kKscOff = kRawLiveOff + (INT8 ? 16 : 0);
   static constexpr int kVscOff = kKscOff + (INT8 ? kScRing * kN * 4 : 0);
   static constexpr int kExpOff = kVscOff + (INT8 ? kScRing * kN * 4 : 0);
   static constexpr int kBadOff = kExpOff + 4 * kScRing;
-  static constexpr int kBarOff = kBadOff + 4 * kBadRing;
+  static constexpr int kBarOff = kBadOff + 8;
   // barriers
   static constexpr int kBarQ = 0;                    // [tile]
   static constexpr int kBarS = 2;                    // [tile][buffer]
@@ -99,8 +99,7 @@ struct Cfg {
   static constexpr int kBarRawFull = kBarEmpty + kSlots;
   static constexpr int kBarRawEmpty = kBarRawFull + kRawSlots;
   static constexpr int kBarSc = kBarRawEmpty + kRawSlots;  // [kScRing]
-  static constexpr int kBarBad = kBarSc + (INT8 ? kScRing : 0);  // [kBadRing]
-  static constexpr int kBarDrain = kBarBad + kBadRing;
+  static constexpr int kBarDrain = kBarSc + (INT8 ? kScRing : 0);
   static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kSmem = kBarOff + 8 * kNumBars + 16 + 1024;
   static_assert(kSmem + 64 <= 232448, "shared memory");
@@ -114,7 +113,6 @@ struct Segment {
   int nrows, tok0, head0;
   int keys;   // of the item's last row
   int steps;  // of kStep keys (the last tile may have one only)
-  int index;  // segments before it
 };
 
 // Calls f(segment) for this CTA's part of the line, in order, until f
@@ -127,7 +125,6 @@ __device__ __forceinline__ void for_segments(const PagedArgs& p,
   if (cur.b >= p.batch) return;
   Segment s;
   s.g = seq_geom(p, cur.b, false);
-  int index = 0;
   while (cur.b < p.batch) {
     const bool at_end = same_item(cur, end);
     s.units = line.units(p, s.g, cur.qt);
@@ -140,12 +137,29 @@ __device__ __forceinline__ void for_segments(const PagedArgs& p,
       s.head0 = cur.kvh * p.group + line.first_head(cur.qt);
       s.keys = line.keys(p, s.g, cur.qt);
       s.steps = min(2 * s.ub, max(1, (s.keys + kStep - 1) / kStep)) - 2 * s.ua;
-      s.index = index++;
       if (!f(s, cur.b)) return;
     }
     if (at_end) return;
     line.next(p, s.g, cur);
   }
+}
+
+// The first of sequence b's keys [lo, hi) that lies on a page out of range,
+// kNoBadKey when none does; by a converged warp.
+__device__ __forceinline__ int first_bad_key(const PagedArgs& p, int b, int lo,
+                                          int hi, int lane) {
+  const int32_t* trow = p.page_table + b * p.table_stride;
+#pragma unroll 1
+  for (int i = lo >> p.page_shift; lo < hi && i <= (hi - 1) >> p.page_shift; i += 32) {
+    bool bad = false;
+    if (i + lane <= (hi - 1) >> p.page_shift) {
+      const int id = trow[i + lane];
+      bad = id < 0 || id >= p.num_pages;
+    }
+    const unsigned any = __ballot_sync(0xffffffffu, bad);
+    if (any) return max(lo, (i + __ffs(any) - 1) << p.page_shift);
+  }
+  return kNoBadKey;
 }
 
 // One key row of codes (D bytes at row r of `src`, swizzled) -> 16-bit row r
@@ -189,7 +203,12 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
   float* ksc = reinterpret_cast<float*>(smem + C::kKscOff);
   float* vsc = reinterpret_cast<float*>(smem + C::kVscOff);
   volatile float* vexp = reinterpret_cast<volatile float*>(smem + C::kExpOff);
-  volatile int* bad_ring = reinterpret_cast<volatile int*>(smem + C::kBadOff);
+  // set once the producer has met a bad page, and never cleared: whoever
+  // finds it set looks at the pages of its own keys (first_bad_key)
+  volatile int* bad_seen = reinterpret_cast<volatile int*>(smem + C::kBadOff);
+  // INT8: keys of a raw tile before its end and its first bad page: the V
+  // behind them counts for no row that is written
+  volatile int* raw_live = reinterpret_cast<volatile int*>(smem + C::kRawLiveOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -217,11 +236,10 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
         mbar_init(&bars[C::kBarSc + s], 4);
       }
     }
-    for (int s = 0; s < kBadRing; ++s)
-      mbar_init(&bars[C::kBarBad + s], 8);  // one arrival per softmax warp
     mbar_init(&bars[C::kBarDrain], 1);
     mbar_init(&bars[C::kBarDrain + 1], 1);
     *abort_flag = 0;
+    *bad_seen = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
@@ -271,16 +289,6 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       uint32_t idx = 0;  // tiles loaded
       bool ok = true;
       for_segments(p, line, begin, end, [&](const Segment& s, int b) {
-        // The entry is free once every softmax warp has read it.  (Segments of
-        // one query tile leave the other tile's warps behind; only this keeps
-        // their lead within the ring.)
-        if (s.index >= kBadRing &&
-            !wait(C::kBarBad + s.index % kBadRing, s.index / kBadRing - 1)) {
-          ok = false;
-          return false;
-        }
-        if (lane == 0) bad_ring[s.index % kBadRing] = 0;
-        __syncwarp();
         const int32_t* trow = p.page_table + b * p.table_stride;
         auto loads = [&](int n) {  // this lane has a piece of tile n
           return piece * bt < kN && n * kN + piece * bt < s.g.len;
@@ -293,12 +301,17 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
           int id = id_next;
           if (n + 1 < s.ub) id_next = page_of(n + 1);
           const bool load = loads(n);
-          if (load && (id < 0 || id >= p.num_pages)) {
+          // Rows that see no key of a bad page are computed, so V has to be
+          // finite there: it reads as zeros (the box lies outside the map), or
+          // for INT8 as another page whose V scales the converters clear.
+          const bool bad = load && (id < 0 || id >= p.num_pages);
+          if (bad) {
             report_status(p.status, kStatusBadPages);
-            bad_ring[s.index % kBadRing] = 1;
-            id = 0;
+            *bad_seen = 1;
+            id = INT8 ? 0 : p.num_pages;
           }
           const int live = min(kN, s.g.len - n * kN);
+          const unsigned bad_lanes = __ballot_sync(0xffffffffu, bad);
           const uint32_t pieces = live > 0 ? (live + bt - 1) >> bt_shift : 0;
           const uint32_t bytes = pieces * bt * (INT8 ? D : D * 2);
           const int slot_key = (n * kN + piece * bt) & ((1 << p.page_shift) - 1);
@@ -309,8 +322,12 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
               ok = false;
               break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(
+            if (lane == 0) {
+              if (INT8 && kv == 0)
+                raw_live[st] = bad_lanes ? (__ffs(bad_lanes) - 1) * bt : live;
+              mbar_arrive_expect_tx(
                   &bars[kFull + st], bytes + (INT8 && kv == 0 ? pieces * bt * 8 : 0));
+            }
             __syncwarp();
             if (load) {
               const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
@@ -489,10 +506,10 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
             }
             const float* sc =
                 reinterpret_cast<const float*>(smem + C::kRawScOff) + raw * 2 * kN;
-            const int live = s.g.len - n * kN;
             uint8_t* dst = ring + st * C::kTile;
             const uint8_t* src = smem + C::kRawOff + raw * C::kRaw;
             if (kv == 0) {
+              const int live = raw_live[raw];
               const float* sv = sc + kN;
               float top = 0.0f;
 #pragma unroll
@@ -543,10 +560,9 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
     uint32_t gs = 0;    // steps of this query tile so far
     uint32_t tile = 0;  // key tiles of earlier segments
     bool ok = true;
-    for_segments(p, line, begin, end, [&](const Segment& s, int) {
+    for_segments(p, line, begin, end, [&](const Segment& s, int b) {
       if (t * kM >= s.nrows) {
         tile += s.ub - s.ua;
-        if (lane == 0) mbar_arrive(&bars[C::kBarBad + s.index % kBadRing]);
         return true;
       }
       // ---- Q: D/8 threads a row, 16 bytes each ----
@@ -750,12 +766,15 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       if (!wait(C::kBarO + 2 * t + ((gs - 1) & 1), (gs - 1) >> 1)) return ok = false;
       tc_fence_after();
       const bool whole = s.ua == 0 && s.ub == s.units;
-      const bool bad = bad_ring[s.index % kBadRing] != 0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[C::kBarBad + s.index % kBadRing]);
+      int bad_key = kNoBadKey;
+      if (__any_sync(0xffffffffu, *bad_seen))
+        bad_key = first_bad_key(p, b, s.ua * kN, min(s.ub * kN, s.g.len), lane);
       const int slot = 2 * blockIdx.x + (s.ua == 0 ? 1 : 0);
-      const bool live = row < s.nrows && !(whole && bad);
-      const int tok = s.g.start + s.tok0 + row / p.group;
+      // (a partial result is judged by the merge, which knows all pieces)
+      const int new_tok = s.tok0 + row / p.group;
+      const bool live = row < s.nrows &&
+                        !(whole && keys_of_token(p, s.g, new_tok) > bad_key);
+      const int tok = s.g.start + new_tok;
       const int h = s.head0 + row % p.group;
       float f = 1.0f;  // O of the exact weights, at the scale of V
       if (INT8) f = inv > 0.0f ? round_off(l_wgt, l_rnd) / inv : 0.0f;
@@ -802,9 +821,9 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       }
       if (!whole && threadIdx.x == 0) {
         p.head[2 * slot] =
-            make_int4(1, s.ub == s.units ? 1 : 0, bad ? 1 : 0, s.nrows);
-        p.head[2 * slot + 1] =
-            make_int4(s.g.start + s.tok0, s.head0, p.group, 0);
+            make_int4(1, s.ub == s.units ? 1 : 0, bad_key, s.nrows);
+        p.head[2 * slot + 1] = make_int4(s.g.start + s.tok0, s.head0, p.group,
+                                         limit_of_token(p, s.g, s.tok0));
       }
       tc_fence_before();  // these reads come before the next segment's MMAs
       return true;

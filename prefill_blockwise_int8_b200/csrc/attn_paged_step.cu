@@ -122,14 +122,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
   const uint32_t ring_a = smem_u32(ring);
   uint8_t* scales = smem + C::kScaleOff + warp * C::kSlots * C::kScale;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * C::kSlots;
-  __shared__ int s_bad;
+  __shared__ int s_bad;  // the item's first key on a bad page; -1: a wait ran out
   if (lane == 0) {
     for (int s = 0; s < C::kSlots; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
   }
-  if (threadIdx.x == 0) s_bad = 0;
+  if (threadIdx.x == 0) s_bad = kNoBadKey;
   pdl_wait();
   clear_headers(p);
   pdl_launch();
@@ -178,21 +178,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
     const int box_shift = min(p.page_shift, G == 32 ? 5 : 4);
     const int ppg_shift = (G == 32 ? 5 : 4) - box_shift;
     int pid = 0, pid_base = -32;
-    bool bad_page = false;
+    // keys whose V counts: the rows that see a bad page are not written, so
+    // from its first key on V may be anything finite, as behind the end
+    int vlen = g.len;
     auto fetch_pids = [&](int base) {
       pid_base = base;
       const int i = base + lane;
       const long long key = k0 + static_cast<long long>(i >> ppg_shift) * C::kUnit +
                             ((i & ((1 << ppg_shift) - 1)) << box_shift);
+      int bad = kNoBadKey;
       pid = 0;
       if (i >> ppg_shift < nst && key < g.len) {
         pid = trow[key >> p.page_shift];
         if (pid < 0 || pid >= p.num_pages) {
-          bad_page = true;
+          bad = static_cast<int>(key);
+          atomicMin(&s_bad, bad);
           report_status(p.status, kStatusBadPages);
           pid = 0;
         }
       }
+      vlen = min(vlen, __reduce_min_sync(0xffffffffu, bad));
     };
     auto issue = [&](int i) {
       const int first = i << ppg_shift;
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
         // the largest live V scale (slots past the end may hold anything)
         const float v =
             lane < G ? __uint_as_float(lds32(sa + G * 4 + 4 * (lane & (G - 1)))) : 0.0f;
-        svm = key0 + lane < g.len ? fabsf(v) : 0.0f;
+        svm = key0 + lane < vlen ? fabsf(v) : 0.0f;
         grow |= inv == 0.0f ? svm > 0.0f : svm * inv > 32.0f;
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
       // P; a row that has seen no key keeps m = -inf and P = 0
       const float mu[2] = {m[0] == -CUDART_INF_F ? 0.0f : m[0],
                            m[1] == -CUDART_INF_F ? 0.0f : m[1]};
-      const bool tail = key0 + G > g.len;
+      const bool tail = key0 + G > vlen;
 #pragma unroll
       for (int h = 0; h < G / 16; ++h) {
         uint32_t pf[4];
@@ -407,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
             va_ = __uint_as_float(lds32(sa + G * 4 + (8 * j + ca) * 4)) * inv;
             vb_ = __uint_as_float(lds32(sa + G * 4 + (8 * j + cb) * 4)) * inv;
             if (tail) {  // P = 0 times the scale of a slot past the end is 0
-              if (key0 + 8 * j + ca >= g.len) va_ = 0.0f;
-              if (key0 + 8 * j + cb >= g.len) vb_ = 0.0f;
+              if (key0 + 8 * j + ca >= vlen) va_ = 0.0f;
+              if (key0 + 8 * j + cb >= vlen) vb_ = 0.0f;
             }
           }
           float e4[4];
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
           // V rows past the sequence's end may hold NaN: cleared in registers
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (tail) {
-            const int live = g.len - key0 - 16 * h;  // keys 2 q4, + 1, + 8, + 9
+            const int live = vlen - key0 - 16 * h;  // keys 2 q4, + 1, + 8, + 9
             auto keep = [&](int k) {
               return (k < live ? 0x0000ffffu : 0u) | (k + 1 < live ? 0xffff0000u : 0u);
             };
@@ -499,8 +504,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
       for (; consumed < issued; ++consumed)
         mbar_wait(&bars[consumed % C::kSlots], (consumed / C::kSlots) & 1, nullptr);
     }
-    const bool any_bad = __any_sync(0xffffffffu, bad_page) || dead;
-
     // ---- the four warps' results merge through their own rings ----
     float* mine = reinterpret_cast<float*>(ring);
     float back[2];  // O of the exact weights, INT8: back to the scale of V
@@ -534,9 +537,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
         row[D + 1] = l[r];
       }
     }
-    if (any_bad && lane == 0) s_bad = 1;
+    if (dead) atomicMin(&s_bad, -1);
     __syncthreads();
-    const bool bad = s_bad != 0;
+    const int bad = s_bad;
     const bool whole = ua == 0 && ub == units;
     const int slot = 2 * blockIdx.x + (ua == 0 ? 1 : 0);
     // thread: row threadIdx / 8, channels 4 (threadIdx % 8) + 32 k
@@ -558,7 +561,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
         f[w] = ex2_approx(mw[w] - mz);
         lt += f[w] * rows[w][D + 1];
       }
-      if (r < nrows && !(whole && bad)) {
+      // (a partial result is judged by the merge, which knows all pieces)
+      if (r < nrows &&
+          !(whole && keys_of_token(p, g, tok0 + r / p.group) > bad)) {
         const int tok = g.start + tok0 + r / p.group;
         const int h = head0 + r % p.group;
         const float il = 1.0f / lt;
@@ -597,13 +602,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
       }
     }
     if (!whole && threadIdx.x == 0) {
-      p.head[2 * slot] = make_int4(1, ub == units ? 1 : 0, bad ? 1 : 0, nrows);
-      p.head[2 * slot + 1] = make_int4(g.start + tok0, head0, p.group, 0);
+      p.head[2 * slot] = make_int4(1, ub == units ? 1 : 0, bad, nrows);
+      p.head[2 * slot + 1] = make_int4(g.start + tok0, head0, p.group,
+                                       limit_of_token(p, g, tok0));
     }
     // the rings take TMA writes again: order the generic accesses before
     fence_proxy_async_smem();
     __syncthreads();
-    if (threadIdx.x == 0) s_bad = 0;
+    if (threadIdx.x == 0) s_bad = kNoBadKey;
     __syncthreads();
 
     if (at_end) break;

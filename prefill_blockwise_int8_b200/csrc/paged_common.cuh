@@ -36,8 +36,9 @@ __device__ __forceinline__ bool find_part(const PagedArgs& p, const L& line,
 // Partial results.  Slot 2 c: the item that began in an earlier block and
 // goes on in (or ends with) block c; slot 2 c + 1: the item that begins in
 // block c and goes on.  A slot holds R rows of {O[D] unnormalised, max (base
-// 2), sum, -, -} and a header {used, the item ends here, bad, rows} {first
-// token row, first query head, group, -}.
+// 2), sum, -, -} and a header {used, the item ends here, first key on a bad
+// page, rows} {first token row, first query head, group, the first token's
+// limit_of_token}.
 // ---------------------------------------------------------------------------
 
 template <int D>
@@ -86,6 +87,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 constexpr float kNone = -__builtin_huge_valf();  // maximum of no keys
+constexpr int kNoBadKey = 0x7fffffff;            // no key is on a bad page
 
 // Running maximum m, sum l and output o of key ranges, added as
 // m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), o likewise.
@@ -130,7 +132,8 @@ __global__ void __launch_bounds__(32 * W * ROWS)
   const int4 it = p.head[2 * (2 * c + 1) + 1];
   Acc<V> acc;
   acc.clear();
-  bool bad = h.z != 0, done = false;
+  int bad_key = h.z;
+  bool done = false;
   auto load = [&](int slot, float& m, float& l, float (&o)[V]) {
     const float* x = part_row<D, R>(p, slot, r);
     m = x[D];
@@ -155,12 +158,12 @@ __global__ void __launch_bounds__(32 * W * ROWS)
     if (b0 + lane < blocks) n = p.head[4 * (b0 + lane)];
     unsigned used = __ballot_sync(0xffffffffu, n.x != 0);
     const unsigned ends = __ballot_sync(0xffffffffu, n.x != 0 && n.y != 0);
-    const unsigned bads = __ballot_sync(0xffffffffu, n.x != 0 && n.z != 0);
     if (ends) {
       used &= 0xffffffffu >> (32 - __ffs(ends));
       done = true;
     }
-    bad |= (bads & used) != 0;
+    bad_key = min(bad_key, __reduce_min_sync(0xffffffffu, (used >> lane) & 1
+                                                              ? n.z : kNoBadKey));
     while (used) {
       float m[4], l[4], o[4][V];
       int got = 0;
@@ -204,7 +207,9 @@ __global__ void __launch_bounds__(32 * W * ROWS)
       acc.add(t[D], t[D + 1], o);
     }
   }
-  if (bad || !done || !row) return;
+  if (!done || !row) return;
+  // a row that sees a key of a bad page keeps its outputs
+  if (it.w + (p.causal ? r / it.z : 0) > bad_key) return;
   const int tok = it.x + r / it.z;
   const int hq = it.y + r % it.z;
   const float il = 1.0f / acc.l;

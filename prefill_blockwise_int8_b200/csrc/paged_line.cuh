@@ -31,10 +31,14 @@ __device__ __forceinline__ SeqGeom seq_geom(const PagedArgs& p, int b,
   return SeqGeom{start, end - start, len};
 }
 
-// Keys that new token i sees.
+// Keys that new token i sees: those below this position, none when negative.
+__device__ __forceinline__ int limit_of_token(const PagedArgs& p,
+                                              const SeqGeom& g, int i) {
+  return p.causal ? g.len - g.n + i + 1 : g.len;
+}
 __device__ __forceinline__ int keys_of_token(const PagedArgs& p,
                                              const SeqGeom& g, int i) {
-  return p.causal ? max(0, g.len - g.n + i + 1) : g.len;
+  return max(0, limit_of_token(p, g, i));
 }
 
 // An item of work (a sequence, a KV head and a tile of at most R packed rows

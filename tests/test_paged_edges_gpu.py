@@ -128,3 +128,42 @@ def test_attn_paged_bad_pages_before_many_short_segments(kv):
     hit = hit.cuda()
     assert torch.equal(out[~hit], good[~hit]) and torch.isfinite(good).all()
     assert (out[hit] == 7).all()
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+@pytest.mark.parametrize("new,lens,page,bad", [
+    (16, [600, 300], 16, {0: [37], 1: [18, 17]}),    # step kernel
+    (2, [97, 5985], 32, {0: [3], 1: [187]}),         # over several blocks
+    (100, [600, 300], 16, {0: [36, 33], 1: [14]}),   # chunk kernel
+    (300, [1000, 6000], 64, {0: [12], 1: [91, 90]}),
+    (300, [700, 290], 128, {0: [4], 1: [1]}),        # rows without keys
+])
+def test_attn_paged_rows_below_a_bad_page(new, lens, page, bad, kv):
+    # causal rows that see no key of a bad page are computed, the rest keep
+    # their outputs
+    c = Cache(lens, [new] * 2, 1, 64, page, torch.float16, kv == "int8", seed=91)
+    q = torch.randn((2 * new, 1, 64), generator=_gen(92)).half()
+    k, v, table, cu, ln, sc = c.device()
+    limit = torch.zeros(2 * new, dtype=torch.long)   # keys of each row
+    first = torch.zeros(2 * new, dtype=torch.long)   # first bad key
+    for b, n in enumerate(lens):
+        for x in bad[b]:
+            table[b, x] = -5 if x % 2 else 1 << 29
+        limit[b * new:(b + 1) * new] = torch.arange(n - new + 1, n + 1)
+        first[b * new:(b + 1) * new] = min(bad[b]) * page
+    hit = limit > first
+    assert hit.any() and (~hit).any()
+    out = torch.full((2 * new, 1, 64), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((1, 2 * new), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tm.tilemix_attn_paged(q.cuda(), k, v, table, cu, ln, new, max(lens), out=out,
+                          lse=lse, status=status, **sc)
+    assert int(status.item()) == BAD_PAGES
+    want, wl, tol = oracle.attn(q, c.k, c.v, c.table, c.cu, c.lens,
+                                k_scale=c.ks, v_scale=c.vs)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert (out[hit] == 7).all() and (lse[:, hit] == 7).all()
+    assert ((out - want).abs()[~hit] <= tol[~hit]).all()
+    seen = ~hit & ~torch.isinf(wl[0])
+    assert ((lse - wl).abs()[:, seen] <= 2e-5 * (1 + wl[:, seen].abs())).all()
+    assert torch.isinf(lse[:, ~hit & ~seen]).all()
