@@ -81,7 +81,8 @@ enum { TILEMIX_FP16 = 0, TILEMIX_BF16 = 1 };
  * not read (may be NULL).  TILEMIX_KV_FP16 only. */
 #define TILEMIX_FLAG_QUANT_ON_CHIP 2u
 
-/* Test only: the kernel withholds the first V tile of every CTA, so the
+/* Test only: the kernel withholds the first V tile of every CTA (paged
+ * attention: the completion of a first tile), so the
  * consumers' bounded pipeline wait expires (after about 2 s): the call
  * reports TILEMIX_ERR_TIMEOUT in *status, writes no defined output, and the
  * context stays usable.  It exercises the timeout path; no fault, trap or
@@ -600,6 +601,7 @@ typedef struct {
   int head_dim;              /* 64 or 128                                   */
   int num_pages, page_size, max_pages;
   float softmax_scale;       /* <= 0 means 1 / sqrt(head_dim)               */
+  uint32_t flags;            /* 0, or TILEMIX_FLAG_TEST_EXPIRE_WAIT         */
   void* out;                 /* [T, hq, d] contiguous                       */
   float* lse;                /* optional fp32 [hq, T]: natural-log LSE      */
   void* workspace;           /* dev scratch, 16-byte aligned; see below     */

@@ -171,7 +171,7 @@ class AttnPagedParams(C.Structure):
         ("hq", C.c_int), ("hkv", C.c_int), ("head_dim", C.c_int),
         ("num_pages", C.c_int), ("page_size", C.c_int),
         ("max_pages", C.c_int), ("softmax_scale", C.c_float),
-        ("out", C.c_void_p), ("lse", C.c_void_p), ("workspace", C.c_void_p),
+        ("flags", C.c_uint32), ("out", C.c_void_p), ("lse", C.c_void_p), ("workspace", C.c_void_p),
         ("workspace_bytes", C.c_size_t), ("status", C.c_void_p),
     ]
 
@@ -898,7 +898,8 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
                        max_q_len: int, max_kv_len: int, *, k_scale=None,
                        v_scale=None, causal: bool = True,
                        softmax_scale: float = 0.0, out=None, lse=None,
-                       workspace=None, status=None, stream=None):
+                       workspace=None, status=None,
+                       test_expire_wait: bool = False, stream=None):
     """Attention of the new tokens q [T, hq, d] (fp16 or bf16) over the paged
     cache: kv_lens int32 [B] counts each sequence's keys, the new tokens' own
     among them when `causal`.  max_q_len and max_kv_len bound the sequences'
@@ -915,7 +916,8 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
                 q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
                 max_q_len, max_kv_len, k_scale=k_scale, v_scale=v_scale,
                 causal=causal, softmax_scale=softmax_scale, out=out, lse=lse,
-                workspace=workspace, status=status)
+                workspace=workspace, status=status,
+                test_expire_wait=test_expire_wait)
     _check_device(index, "k_pages v_pages page_table cu_seqlens kv_lens "
                   "k_scale v_scale out lse workspace status", k_pages, v_pages,
                   page_table, cu_seqlens, kv_lens, k_scale, v_scale, out, lse,
@@ -945,7 +947,9 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
           _pack_attn(code, fmt, 1 if causal else 0, q.data_ptr(), qt, qh,
                      k_pages.data_ptr(), v_pages.data_ptr(), sp, st, sh, ks, vs,
                      table, ts, cu, lens, batch, t, max_q_len, max_kv_len, hq,
-                     hkv, d, n, page, width, softmax_scale, out.data_ptr(), lp,
+                     hkv, d, n, page, width, softmax_scale,
+                     FLAG_TEST_EXPIRE_WAIT if test_expire_wait else 0,
+                     out.data_ptr(), lp,
                      workspace.data_ptr(),
                      workspace.numel() * workspace.element_size(),
                      _status_ptr(status)), index)

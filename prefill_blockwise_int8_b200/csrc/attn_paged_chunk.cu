@@ -223,13 +223,15 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
       mbar_init(&bars[C::kBarO + 2 * t], 1);
       mbar_init(&bars[C::kBarO + 2 * t + 1], 1);
     }
+    // the timeout path's test: one arrival more than ever comes for the first V
+    const int held = p.test_expire_wait ? 1 : 0;
     for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(&bars[C::kBarFull + s], INT8 ? 4 : 1);
+      mbar_init(&bars[C::kBarFull + s], INT8 ? 4 : s == 1 ? 1 + held : 1);
       mbar_init(&bars[C::kBarEmpty + s], 2);  // both MMA warps
     }
     if (INT8) {
       for (int s = 0; s < C::kRawSlots; ++s) {
-        mbar_init(&bars[C::kBarRawFull + s], 1);
+        mbar_init(&bars[C::kBarRawFull + s], s == 1 ? 1 + held : 1);
         mbar_init(&bars[C::kBarRawEmpty + s], 4);
       }
       for (int s = 0; s < kScRing; ++s) {
@@ -355,11 +357,11 @@ __global__ void __launch_bounds__(Cfg<D, BF16, INT8>::kThreads, 1)
         return ok;
       });
       if (!ok) fail();
-      // copies in flight land (bounded) before the CTA may exit
+      // Copies in flight land (bounded) before the CTA may exit, whoever
+      // gave up: this warp may have issued its last one by then.
       const uint32_t first = idx > kStages ? idx - kStages : 0;
-      if (!ok)
-        for (uint32_t i = first; i < idx; ++i)
-          mbar_wait(&bars[kFull + i % kStages], (i / kStages) & 1, nullptr);
+      for (uint32_t i = first; i < idx; ++i)
+        mbar_wait(&bars[kFull + i % kStages], (i / kStages) & 1, nullptr);
     } else if (warp == kWarpMma || warp == kWarpMma + 1) {
       // =================== MMA issuers ===================
       // One warp per query tile: a wait between two products costs about 100

@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, INT8>)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * C::kSlots;
   __shared__ int s_bad;  // the item's first key on a bad page; -1: a wait ran out
   if (lane == 0) {
-    for (int s = 0; s < C::kSlots; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < C::kSlots; ++s)
+      mbar_init(&bars[s], s == 0 && p.test_expire_wait ? 2 : 1);
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);

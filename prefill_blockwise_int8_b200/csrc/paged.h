@@ -64,6 +64,7 @@ struct PagedArgs {
   int num_pages, page_shift, max_pages;
   int causal;
   float scale_log2;  // softmax scale * log2(e)
+  int test_expire_wait;  // a first tile's barrier never completes
   uint16_t* out;
   float* lse;
   int32_t* status;

@@ -376,6 +376,8 @@ tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
   if ((a->dtype != TILEMIX_FP16 && a->dtype != TILEMIX_BF16) ||
       (a->causal != 0 && a->causal != 1))
     return fail(TILEMIX_ERR_INVALID_ARG, "%s: bad dtype or causal", where);
+  if (a->flags & ~TILEMIX_FLAG_TEST_EXPIRE_WAIT)
+    return fail(TILEMIX_ERR_INVALID_ARG, "%s: bad flags 0x%x", where, a->flags);
   tilemix_status st = check_cache(
       where, a->kv_format, a->k_pages, a->v_pages, a->page_stride,
       a->token_stride, a->head_stride, a->k_scale, a->v_scale, a->page_table,
@@ -449,6 +451,7 @@ tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
   const float scale =
       a->softmax_scale > 0.0f ? a->softmax_scale : 1.0f / std::sqrt(float(d));
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.test_expire_wait = (a->flags & TILEMIX_FLAG_TEST_EXPIRE_WAIT) ? 1 : 0;
   p.out = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
   p.status = a->status;

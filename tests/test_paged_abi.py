@@ -317,3 +317,11 @@ def test_oracle_attention_is_dense_attention(causal, int8):
     want = torch.einsum("hij,jhd->ihd", s.softmax(-1), vd)
     assert torch.allclose(out, want) and torch.allclose(lse, s.logsumexp(-1))
     assert (tol > 0).all()
+
+
+def test_attn_flags():
+    assert accepted(lambda: attn(flags=tm.FLAG_TEST_EXPIRE_WAIT))
+    for bad in (1, 2, 8, 1 << 31):
+        assert attn(flags=bad) == INVALID and "flags" in tm.tilemix_last_error()
+    # the field fills what was padding: no other one moved
+    assert C.sizeof(tm.AttnPagedParams) == 216

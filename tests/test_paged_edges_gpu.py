@@ -167,3 +167,33 @@ def test_attn_paged_rows_below_a_bad_page(new, lens, page, bad, kv):
     seen = ~hit & ~torch.isinf(wl[0])
     assert ((lse - wl).abs()[:, seen] <= 2e-5 * (1 + wl[:, seen].abs())).all()
     assert torch.isinf(lse[:, ~hit & ~seen]).all()
+
+
+# ---------------------------------------------------------------------------
+# a wait that runs out
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv,new,n", [("same", 1, 700), ("int8", 1, 700),
+                                      ("same", 40, 100), ("same", 40, 5000),
+                                      ("int8", 40, 100), ("int8", 40, 5000)])
+def test_attn_paged_expired_wait_reports_timeout(kv, new, n):
+    # a first tile's barrier never completes: its bounded wait expires (2 s),
+    # every copy in flight lands, rows of the blocks that gave up are not
+    # written, and the next call on the same context and workspace is right.
+    # With 100 keys the loads have all been issued when the wait runs out.
+    c = Cache([n, n], [new, new], 1, 64, 64, torch.float16, kv == "int8", seed=5)
+    q = torch.randn((2 * new, 2, 64), generator=_gen(6)).half()
+    k, v, table, cu, lens, sc = c.device()
+    ws = torch.empty(tm.tilemix_attn_paged_workspace_bytes(new, 2, 1, 64),
+                     dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((2 * new, 2, 64), 7.0, dtype=torch.float16, device="cuda")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    tm.tilemix_attn_paged(q.cuda(), k, v, table, cu, lens, new, n, out=out,
+                          workspace=ws, status=status, test_expire_wait=True, **sc)
+    end.record()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 4 and start.elapsed_time(end) < 30e3
+    assert (out == 7).all()
+    _check_attn(c, q, True, workspace=ws)
