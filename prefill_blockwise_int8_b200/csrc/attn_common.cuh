@@ -89,19 +89,21 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 
 // 2^x of two values on the FMA pipe: x = n + f with n the nearest integer
 // (read off the low bits of x + 1.5 2^23), 2^f as 1 + f q(f), q the least
-// relative maximum error fit on [-1/2, 1/2] (2.9e-6 in fp32), and n added to
-// the exponent.  x <= -127 (-inf too) gives exactly 0, since q drops out at
-// f = 0; x < 128 is required.
+// relative maximum error fit on [-1/2, 1/2], and n added to the exponent.  Off
+// by 1.7e-7 in fp32, as little as the exponential unit (with one degree less
+// by 2.9e-6).  x <= -127 (-inf too) gives exactly 0, since q drops out at f =
+// 0; x < 128 is required.
 __device__ __forceinline__ float2 ex2_poly2(float2 x) {
   x.x = fmaxf(x.x, -127.0f);
   x.y = fmaxf(x.y, -127.0f);
   const float2 t = __fadd2_rn(x, make_float2(kIntBias, kIntBias));
   const float2 n = __fadd2_rn(t, make_float2(-kIntBias, -kIntBias));
   const float2 f = __ffma2_rn(n, make_float2(-1.0f, -1.0f), x);
-  float2 p = __ffma2_rn(f, make_float2(0x1.3a02a8p-7f, 0x1.3a02a8p-7f),
-                        make_float2(0x1.c9fc40p-5f, 0x1.c9fc40p-5f));
-  p = __ffma2_rn(f, p, make_float2(0x1.ec0378p-3f, 0x1.ec0378p-3f));
-  p = __ffma2_rn(f, p, make_float2(0x1.62e12cp-1f, 0x1.62e12cp-1f));
+  float2 p = __ffma2_rn(f, make_float2(0x1.5bba14p-10f, 0x1.5bba14p-10f),
+                        make_float2(0x1.3cea88p-7f, 0x1.3cea88p-7f));
+  p = __ffma2_rn(f, p, make_float2(0x1.c6b752p-5f, 0x1.c6b752p-5f));
+  p = __ffma2_rn(f, p, make_float2(0x1.ebf9bcp-3f, 0x1.ebf9bcp-3f));
+  p = __ffma2_rn(f, p, make_float2(0x1.62e42ap-1f, 0x1.62e42ap-1f));
   p = __ffma2_rn(f, p, make_float2(1.0f, 1.0f));
   return make_float2(
       __int_as_float((__float_as_int(t.x) << 23) + __float_as_int(p.x)),
