@@ -569,7 +569,8 @@ typedef struct {
  * multiplication by the rounded reciprocal; tilemix_quantize_blockwise divides,
  * which may differ in the last bit), code = round_half_even(x / scale) with an
  * IEEE fp32 division, scale 0 and codes 0 for a = 0.  A row with NaN or
- * infinity gets codes and a scale of no meaning, other rows are not affected.
+ * infinity gets scale NaN and codes of no meaning, so that what reads it is
+ * NaN; other rows are not affected.
  * Two tokens of one call that map to the same page slot race.
  */
 tilemix_status tilemix_paged_append(const tilemix_append_params* params,

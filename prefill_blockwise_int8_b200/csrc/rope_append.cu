@@ -283,13 +283,15 @@ __global__ void __launch_bounds__(kThreads)
         }
         float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(fa[i]), fabsf(fb[i])));
+        for (int i = 0; i < 8; ++i) m = fmax3_nan(m, fabsf(fa[i]), fabsf(fb[i]));
         // units is 4 or 8 (head_dim 64 or 128): a head's lanes are an aligned
         // group of that many
         for (int o = units >> 1; o > 0; o >>= 1)
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (live && !is_q) {
-          const float sc = __fmul_rn(m, kInv127);
+          // (m - m: 0, but NaN where the row has NaN or infinity, so that what
+          // reads it is NaN)
+          const float sc = __fmaf_rn(m, kInv127, __fsub_rn(m, m));
           const float rcp = m != 0.0f ? __frcp_rn(sc) : 0.0f;
           uint32_t ca[8], cb[8];
           quant_codes8(fa, sc, rcp, ca);

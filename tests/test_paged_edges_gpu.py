@@ -197,3 +197,39 @@ def test_attn_paged_expired_wait_reports_timeout(kv, new, n):
     assert int(status.item()) == 4 and start.elapsed_time(end) < 30e3
     assert (out == 7).all()
     _check_attn(c, q, True, workspace=ws)
+
+
+# ---------------------------------------------------------------------------
+# appending
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rot", [0, 64])
+@pytest.mark.parametrize("new", [3, 1100])   # one and 16 tokens a block
+def test_append_int8_keeps_non_finite_rows_visible(new, rot, dtype):
+    c = Cache([new + 9], [new], 2, 64, 32, dtype, True, seed=3)
+    x = torch.randn((new, 4, 64), generator=_gen(4)).to(dtype)
+    x[0, 0, 5], x[1, 1, 60] = math.nan, math.inf
+    x[1, 2, 0], x[2, 3, 63] = -math.inf, math.nan
+    x[2, 0, 1], x[2, 0, 2] = math.inf, math.nan
+    k, v, table, cu, lens, sc = c.device()
+    freqs = torch.tensor([10000.0 ** (-2.0 * i / rot) for i in range(rot // 2)],
+                         dtype=torch.float64).cuda() if rot else None
+    tm.tilemix_paged_append(x[:, :2].cuda(), x[:, 2:].cuda(), table, cu, lens,
+                            k, v, freqs=freqs, **sc)
+    rows = x.clone()
+    if rot:
+        pos = torch.arange(9, new + 9, dtype=torch.int32).cuda()
+        rows[:, :2] = tm.tilemix_rope(x[:, :2].cuda(), None, pos, freqs)[0].cpu()
+    for t, b, p, pid, slot in oracle.places(c.cu, c.lens, c.table.tolist(), 32):
+        codes = torch.cat((k[pid, slot], v[pid, slot])).cpu()
+        scale = torch.cat((sc["k_scale"][pid, :, slot],
+                           sc["v_scale"][pid, :, slot])).cpu()
+        top = rows[t].float().abs().amax(-1)   # NaN where the row has one
+        bad = ~torch.isfinite(top)
+        assert torch.equal(torch.isnan(scale), bad)
+        want, ws = oracle.quantised(rows[t])
+        assert torch.equal(codes[~bad], want[~bad])
+        assert torch.equal(scale[~bad], ws[~bad])
+        if t == 6:
+            break
