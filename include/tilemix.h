@@ -425,17 +425,19 @@ tilemix_status tilemix_attn_prefill(const tilemix_attn_params* params,
  * never change when later tokens join its page, unlike block scales.
  *
  * New tokens.  cu_seqlens (dev int32 [batch + 1], as for the prefill calls)
- * delimits each sequence's new tokens in the token-major tensors; rows at or
- * past cu_seqlens[batch] are padding, neither read nor written.  kv_lens
- * (dev int32 [batch]) is each sequence's cache length AFTER its new tokens
- * joined; the same array serves the append and the attention.
+ * delimits each sequence's new tokens in the token-major tensors; rows before
+ * cu_seqlens[0] and from cu_seqlens[batch] on are padding, neither read nor
+ * written.  kv_lens (dev int32 [batch]) is each sequence's cache length AFTER
+ * its new tokens joined; the same array serves the append and the attention.
  *
  * Device-side checks (status word): BAD_SEQLENS for a cu_seqlens that
- * decreases or leaves [0, total_tokens], or a kv_lens entry that is negative
- * or above what the table row can hold (or max_kv_len); BAD_PAGES for a page
- * table entry in use outside [0, num_pages).  The sequences (for a bad page:
- * the tokens, or the query rows whose keys reach it) that show the problem
- * keep their outputs as they were; the others are computed.
+ * decreases or leaves [0, total_tokens] (attention: or a sequence of more than
+ * max_q_len tokens) and for a kv_lens entry that is negative or above what the
+ * table row can hold (attention: or above max_kv_len; append: or below the
+ * number of new tokens); BAD_PAGES for a page table entry in use outside [0,
+ * num_pages).  The sequences (for a bad page: the tokens, or the query rows
+ * whose keys reach it) that show the problem keep their outputs as they were;
+ * the others are computed.
  * ---------------------------------------------------------------------------
  */
 

@@ -106,6 +106,13 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int batch,
   return lo;
 }
 
+// What an append refuses a sequence for.
+__device__ __forceinline__ bool bad_sequence(const RopeArgs& p, int start,
+                                             int end, int len) {
+  return start < 0 || end < start || end > p.total_tokens || len < end - start ||
+         len > (static_cast<long long>(p.max_pages) << p.page_shift);
+}
+
 // Where a token's rows go (append): page id and slot, or page < 0.
 struct Place {
   int page, slot, pos;
@@ -124,6 +131,16 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (MODE != 0) {
+    // Block 0 looks every sequence over, those without new tokens included (by
+    // its last warps, which have no token to place in a small call).
+    if (blockIdx.x == 0 && p.status)
+      for (int b = static_cast<int>(threadIdx.x) - kThreads / 2; b < p.batch;
+           b += kThreads / 2) {
+        if (b < 0) break;
+        const int start = p.cu_seqlens[b], end = p.cu_seqlens[b + 1];
+        if (bad_sequence(p, start, end, p.kv_lens[b]))
+          report_status(p.status, kStatusBadSeqlens);
+      }
     // one warp per token finds its sequence and checks its place
     for (int tt = warp; tt < nt; tt += kThreads / 32) {
       const int t = t0 + tt;
@@ -133,10 +150,10 @@ __global__ void __launch_bounds__(kThreads)
         const int start = p.cu_seqlens[b], end = p.cu_seqlens[b + 1];
         const int len = p.kv_lens[b];
         const long long pos = static_cast<long long>(len) - (end - start) + (t - start);
-        if (start < 0 || t < start || t >= end || end > p.total_tokens ||
-            len < end - start ||
-            len > (static_cast<long long>(p.max_pages) << p.page_shift)) {
-          if (lane == 0) report_status(p.status, kStatusBadSeqlens);
+        if (t < start || t >= end || bad_sequence(p, start, end, len)) {
+          // (before the first sequence: padding)
+          if (lane == 0 && !(b == 0 && t < start))
+            report_status(p.status, kStatusBadSeqlens);
         } else {
           const int page =
               p.page_table[b * p.table_stride + (pos >> p.page_shift)];

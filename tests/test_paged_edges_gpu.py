@@ -233,3 +233,54 @@ def test_append_int8_keeps_non_finite_rows_visible(new, rot, dtype):
         assert torch.equal(scale[~bad], ws[~bad])
         if t == 6:
             break
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+@pytest.mark.parametrize("pad", [0, 1200])   # one and several tokens a block
+def test_append_reports_every_bad_sequence(kv, pad):
+    # also where no token is placed by it: a decreasing end, idle sequences
+    c = Cache([40, 50, 30], [6, 4, 0], 2, 64, 16, torch.float16, kv == "int8")
+    x = torch.randn((10 + pad, 2, 64), generator=_gen(7)).half().cuda()
+    _, _, table, cu, lens, _ = c.device()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()
+    for bad_cu, bad_lens, want in [
+            ([0, 6, 10, 10], [40, 50, 30], 0),
+            ([0, 10, 4, 4], [40, 50, 30], BAD_SEQLENS),
+            ([0, 6, 10, 9], [40, 50, 30], BAD_SEQLENS),
+            ([0, 6, 10, 10], [40, 50, -1], BAD_SEQLENS),
+            ([0, 6, 10, 10], [40, 50, 1 << 20], BAD_SEQLENS),
+            ([0, 6, 10, 11 + pad], [40, 50, 30], BAD_SEQLENS),
+            ([-1, 6, 10, 10], [40, 50, 30], BAD_SEQLENS)]:
+        k, v, _, _, _, sc = c.device()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        tm.tilemix_paged_append(x, x, table, i32(bad_cu), i32(bad_lens), k, v,
+                                status=status, **sc)
+        assert int(status.item()) == want, (bad_cu, bad_lens)
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+@pytest.mark.parametrize("new", [3, 600])
+def test_rows_before_the_first_sequence_are_padding(new, kv):
+    c = Cache([new + 7, new + 30], [new, new], 2, 64, 32, torch.float16,
+              kv == "int8", poison=False)
+    x = torch.randn((2 * new + 5, 8, 64), generator=_gen(8)).half().cuda()
+    k, v, table, cu, lens, sc = c.device()
+    k2, v2, _, _, _, sc2 = c.device()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    f = torch.tensor([10000.0 ** (-i / 16.0) for i in range(16)],
+                     dtype=torch.float64).cuda()
+    qo = torch.full((2 * new + 5, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    args = dict(freqs=f, status=status)
+    tm.tilemix_paged_append(x[:, :2], x[:, 2:4], table, cu + 5, lens, k, v,
+                            q=x[:, 4:], q_out=qo, **args, **sc)
+    want = tm.tilemix_paged_append(x[5:, :2], x[5:, 2:4], table, cu, lens, k2, v2,
+                                   q=x[5:, 4:], **args, **sc2)
+    assert int(status.item()) == 0
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    assert (qo[:5] == 7).all() and torch.equal(qo[5:], want)
+    out = torch.full_like(qo, 7.0)
+    tm.tilemix_attn_paged(qo, k, v, table, cu + 5, lens, new, new + 30, out=out,
+                          status=status, **sc)
+    ref = tm.tilemix_attn_paged(want, k, v, table, cu, lens, new, new + 30, **sc)
+    assert int(status.item()) == 0
+    assert (out[:5] == 7).all() and torch.equal(out[5:], ref)
