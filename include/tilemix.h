@@ -417,7 +417,8 @@ tilemix_status tilemix_attn_prefill(const tilemix_attn_params* params,
  * element (page, slot, head, c) lies at
  *   page * page_stride + slot * token_stride + head * head_stride + c
  * (elements; the same strides for K and V), so pages may be laid out token-
- * or head-major, or interleave K and V.  Position p of sequence b lies in
+ * or head-major, or interleave K and V; an append needs pages and their rows
+ * that do not overlap.  Position p of sequence b lies in
  * page page_table[b * table_stride + p / page_size], slot p % page_size.
  * The rest of a table row is never read.  Pages hold the 16-bit type of the
  * call, or INT8 codes (TILEMIX_KV_INT8) with one fp32 scale per (token,
@@ -494,7 +495,8 @@ typedef struct {
   /* [T, hq, d] and [T, hkv, d], channels contiguous, token and head strides
    * in elements (multiples of 8), 16-byte aligned bases.  k may be NULL (hkv
    * is then ignored).  An output equal to its input (same strides) rotates
-   * in place; any other overlap is undefined. */
+   * in place; any other overlap is undefined.  An output's rows lie apart:
+   * one axis steps over all of the other. */
   const void* q;
   const void* k;
   void* q_out;

@@ -32,9 +32,15 @@ bool rows_ok(const void* p, int64_t st, int64_t sh, int unit) {
   return aligned(p, 16) && st % unit == 0 && sh % unit == 0 && st >= 0 && sh >= 0;
 }
 
-// An output's rows may not overlap (strides of axes of one are not used).
+// The rows of a page or an output may not overlap: one axis steps over all that
+// the other spans (strides of axes of one are not used).
 bool apart(int64_t st, int64_t sh, int tokens, int heads, int d) {
-  return (tokens <= 1 || st >= d) && (heads <= 1 || sh >= d);
+  if (tokens <= 1) return heads <= 1 || sh >= d;
+  if (heads <= 1) return st >= d;
+  // (in double: a stride may be anything)
+  const double span_t = d + static_cast<double>(st) * (tokens - 1);
+  const double span_h = d + static_cast<double>(sh) * (heads - 1);
+  return st < sh ? st >= d && sh >= span_t : sh >= d && st >= span_h;
 }
 
 // Shared checks of the cache arguments.
@@ -238,7 +244,7 @@ tilemix_status tilemix_rope(const tilemix_rope_params* a, tilemix_stream_t strea
   if (!apart(a->q_out_stride_t, a->q_out_stride_h, a->total_tokens, a->hq, a->head_dim) ||
       (a->k && !apart(a->k_out_stride_t, a->k_out_stride_h, a->total_tokens,
                       a->hkv, a->head_dim)))
-    return fail(TILEMIX_ERR_INVALID_ARG, "rope: output strides below head_dim");
+    return fail(TILEMIX_ERR_INVALID_ARG, "rope: output rows overlap");
   tilemix_status d = check_device();
   if (d != TILEMIX_OK) return d;
   tilemix::RopeArgs r;
@@ -308,7 +314,9 @@ tilemix_status tilemix_paged_append(const tilemix_append_params* a,
                 "elements", where);
   if (a->q && !apart(a->q_out_stride_t, a->q_out_stride_h, a->total_tokens, a->hq,
                      a->head_dim))
-    return fail(TILEMIX_ERR_INVALID_ARG, "%s: q_out strides below head_dim", where);
+    return fail(TILEMIX_ERR_INVALID_ARG, "%s: rows of q_out overlap", where);
+  if (!apart(a->token_stride, a->head_stride, a->page_size, a->hkv, a->head_dim))
+    return fail(TILEMIX_ERR_INVALID_ARG, "%s: rows of a page overlap", where);
   tilemix_status d = check_device();
   if (d != TILEMIX_OK) return d;
   tilemix::RopeArgs r;

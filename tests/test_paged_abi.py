@@ -325,3 +325,39 @@ def test_attn_flags():
         assert attn(flags=bad) == INVALID and "flags" in tm.tilemix_last_error()
     # the field fills what was padding: no other one moved
     assert C.sizeof(tm.AttnPagedParams) == 216
+
+
+@pytest.mark.parametrize("over", [
+    dict(q_out_stride_t=128, q_out_stride_h=128),   # row t, h = row t + h
+    dict(q_out_stride_t=256, q_out_stride_h=128),
+    dict(k_out_stride_t=128, k_out_stride_h=256),
+    dict(q_out_stride_t=128, q_out_stride_h=512),
+    dict(q_out_stride_t=1016), dict(k_out_stride_t=248)])
+def test_rope_refuses_outputs_that_overlap(over):
+    assert rope(**over) == INVALID and "overlap" in tm.tilemix_last_error()
+
+
+def test_outputs_may_lie_either_way():
+    assert accepted(lambda: rope(q_out_stride_t=128, q_out_stride_h=5 * 128))
+    assert accepted(lambda: rope(q_out_stride_t=1 << 40, q_out_stride_h=136))
+    assert accepted(lambda: rope(total_tokens=1, q_out_stride_t=0))
+    assert accepted(lambda: rope(hq=1, q_out_stride_h=0, q_out_stride_t=128))
+    # pages: token-major (above), head-major, heads outermost, one page, K and
+    # V interleaved by page, slot or head
+    for sp, st, sh, over in [
+            (16 * 256, 128, 16 * 128, {}), (16 * 128, 128, 30 * 16 * 128, {}),
+            (0, 256, 128, dict(num_pages=1)), (16 * 256, 256, 0, dict(hkv=1)),
+            (2 * 16 * 256, 256, 128, {}), (2 * 16 * 256, 512, 128, {}),
+            (2 * 16 * 256, 512, 256, {})]:
+        assert accepted(lambda: append(page_stride=sp, token_stride=st,
+                                       head_stride=sh, **over))
+
+
+@pytest.mark.parametrize("sp,st,sh", [
+    (16 * 256, 128, 128), (16 * 256, 256, 256), (16 * 256, 248, 128),
+    (16 * 256, 136, 128), (16 * 256, 128, 15 * 128), (16 * 256, 128, 256)])
+def test_append_refuses_pages_that_overlap(sp, st, sh):
+    assert append(page_stride=sp, token_stride=st, head_stride=sh) == INVALID
+    assert "overlap" in tm.tilemix_last_error()
+    # reading them is well defined
+    assert accepted(lambda: attn(page_stride=sp, token_stride=st, head_stride=sh))
