@@ -557,7 +557,8 @@ typedef struct {
   int head_dim;              /* 64 or 128                                   */
   int rot_dim;               /* with freqs: multiple of 16 in [16, head_dim] */
   int num_pages, page_size, max_pages;  /* page_size a power of two in
-                                [16, 256]; max_pages: entries of a table row */
+                                [16, 256]; max_pages: entries of a table row,
+                                max_pages * page_size <= 2^31 - 1024        */
   float attn_factor;         /* 0 = 1                                       */
   int32_t* status;           /* optional                                    */
 } tilemix_append_params;

@@ -65,9 +65,10 @@ tilemix_status check_cache(const char* where, int kv_format, const void* k_pages
     return fail(TILEMIX_ERR_UNSUPPORTED,
                 "%s: page_size %d not a power of two in [16, 256]", where,
                 page_size);
-  if (static_cast<long long>(max_pages) * page_size > 0x7fffffffll)
-    return fail(TILEMIX_ERR_UNSUPPORTED, "%s: max_pages * page_size above 2^31 - 1",
-                where);
+  // positions are int32 and the kernels look up to 1023 keys past the last one
+  if (static_cast<long long>(max_pages) * page_size > (1ll << 31) - 1024)
+    return fail(TILEMIX_ERR_UNSUPPORTED,
+                "%s: max_pages * page_size above 2^31 - 1024", where);
   if (batch == 0 || total_tokens == 0) return ok();
   if (!k_pages || !v_pages || !page_table || !cu_seqlens || !kv_lens ||
       (int8 && (!k_scale || !v_scale)))

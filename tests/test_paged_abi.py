@@ -361,3 +361,12 @@ def test_append_refuses_pages_that_overlap(sp, st, sh):
     assert "overlap" in tm.tilemix_last_error()
     # reading them is well defined
     assert accepted(lambda: attn(page_stride=sp, token_stride=st, head_stride=sh))
+
+
+def test_positions_stay_inside_32_bits():
+    # unit ends and the keys a copy looks ahead are int32 too
+    most = ((1 << 31) - 1024) // 16
+    for call in (append, attn):
+        assert accepted(lambda: call(max_pages=most, table_stride=most))
+        for n in (most + 1, (1 << 27) - 1):
+            assert call(max_pages=n, table_stride=n) == UNSUPPORTED
