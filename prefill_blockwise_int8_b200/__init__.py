@@ -889,7 +889,10 @@ def tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
 @functools.lru_cache(maxsize=256)
 def tilemix_attn_paged_workspace_bytes(max_q_len: int, hq: int, hkv: int,
                                        head_dim: int) -> int:
-    """Bytes of device scratch tilemix_attn_paged needs."""
+    """Bytes of device scratch tilemix_attn_paged needs; 0 for sizes it
+    refuses."""
+    if not all(-1 << 31 <= x < 1 << 31 for x in (max_q_len, hq, hkv, head_dim)):
+        return 0  # (ctypes would pass the low 32 bits)
     return int(lib.tilemix_attn_paged_workspace_bytes(max_q_len, hq, hkv,
                                                       head_dim))
 
@@ -922,6 +925,8 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
                   "k_scale v_scale out lse workspace status", k_pages, v_pages,
                   page_table, cu_seqlens, kv_lens, k_scale, v_scale, out, lse,
                   workspace, status)
+    if not (max_q_len < 1 << 31 and max_kv_len < 1 << 31):
+        raise ValueError("max_q_len and max_kv_len must be below 2^31")
     dtype = q.dtype
     code = _dtype_code(torch, dtype, "q")
     (fmt, sp, st, sh, ks, vs, table, ts, cu, lens, batch, n, page, hkv, d,

@@ -104,6 +104,11 @@ tilemix_status check_heads(const char* where, int hq, int hkv) {
   return ok();
 }
 
+// Packed rows of a sequence are counted in int32.
+bool too_many_rows(int max_q_len, int group) {
+  return static_cast<long long>(max_q_len) * group > (1ll << 30);
+}
+
 // Which attention kernel: the step kernel reads the cache once per 16 packed
 // rows, the chunk kernel once per 256 but with more to begin and end.  16
 // sequences of 6000 keys, d 128, step against chunk: 16 rows 50 / 49 us, 24
@@ -366,7 +371,7 @@ tilemix_status tilemix_paged_append(const tilemix_append_params* a,
 size_t tilemix_attn_paged_workspace_bytes(int max_q_len, int hq, int hkv,
                                           int head_dim) {
   if (max_q_len < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || hq / hkv > 128 ||
-      (head_dim != 64 && head_dim != 128))
+      (head_dim != 64 && head_dim != 128) || too_many_rows(max_q_len, hq / hkv))
     return 0;
   // (of 17 to 32 rows either kernel may come: the chunk kernel needs more)
   return use_step(max_q_len, hq / hkv, false)
@@ -399,7 +404,7 @@ tilemix_status tilemix_attn_paged(const tilemix_attn_paged_params* a,
     return fail(TILEMIX_ERR_INVALID_ARG, "%s: bad size", where);
   if (std::isnan(a->softmax_scale) || std::isinf(a->softmax_scale))
     return fail(TILEMIX_ERR_INVALID_ARG, "%s: bad softmax_scale", where);
-  if (static_cast<long long>(a->max_q_len) * (a->hq / a->hkv) > (1ll << 30))
+  if (too_many_rows(a->max_q_len, a->hq / a->hkv))
     return fail(TILEMIX_ERR_UNSUPPORTED, "%s: too many packed query rows", where);
   if (a->batch == 0 || a->total_tokens == 0 || a->max_q_len == 0) return ok();
   if (!a->q || !a->out)

@@ -370,3 +370,14 @@ def test_positions_stay_inside_32_bits():
         assert accepted(lambda: call(max_pages=most, table_stride=most))
         for n in (most + 1, (1 << 27) - 1):
             assert call(max_pages=n, table_stride=n) == UNSUPPORTED
+
+
+def test_sizes_beyond_32_bits():
+    ws = tm.tilemix_attn_paged_workspace_bytes
+    for n in ((1 << 32) + 1, 1 << 31, (1 << 30) // 4 + 1):
+        assert ws(n, 8, 2, 128) == 0
+    assert ws((1 << 30) // 4, 8, 2, 128) > 0
+    assert ws(1, (1 << 32) + 8, 2, 128) == 0
+    q, pages = torch.empty((1, 8, 128)), torch.empty((1, 16, 2, 128))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        tm.tilemix_attn_paged(q, pages, pages, None, None, None, 1 << 31, 1)

@@ -284,3 +284,14 @@ def test_rows_before_the_first_sequence_are_padding(new, kv):
     ref = tm.tilemix_attn_paged(want, k, v, table, cu, lens, new, new + 30, **sc)
     assert int(status.item()) == 0
     assert (out[:5] == 7).all() and torch.equal(out[5:], ref)
+
+
+def test_attn_paged_bounds_beyond_32_bits_are_refused():
+    c = Cache([30], [1], 1, 64, 16, torch.float16, False)
+    k, v, table, cu, lens, _ = c.device()
+    q = torch.zeros((1, 1, 64), dtype=torch.float16, device="cuda")
+    for a, b in ((1 << 31, 30), (1, 1 << 31), ((1 << 32) + 1, 30)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            tm.tilemix_attn_paged(q, k, v, table, cu, lens, a, b)
+    with pytest.raises(tm.TilemixError):
+        tm.tilemix_attn_paged(q, k, v, table, cu, lens, 1 << 30 | 1, 30)
