@@ -759,14 +759,53 @@ def tilemix_rope_frequencies(rot_dim: int, base: float = 10000.0, *,
     return freqs, float(att.value)
 
 
+@functools.lru_cache(maxsize=None)
+def _rope_function():
+    """tilemix_rope as a node of autograd: its gradient is the rotation by the
+    negative angle (with the same attn_factor), so it is one too."""
+    torch = _torch()
+
+    def rows(g):  # a gradient may be expanded, or lie anywhere
+        if g.stride(-1) != 1 or any(s % 8 for s in g.stride()[:2]):
+            g = g.contiguous()
+        return g.clone() if g.data_ptr() % 16 else g
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, freqs, layout, attn_factor, inverse):
+            ctx.save_for_backward(positions, freqs)
+            ctx.how = layout, attn_factor, inverse
+            ctx.set_materialize_grads(False)
+            return tilemix_rope(q, k, positions, freqs, layout=layout,
+                                attn_factor=attn_factor, inverse=inverse)
+
+        @staticmethod
+        def backward(ctx, gq, gk):
+            layout, attn_factor, inverse = ctx.how
+            want = [g is not None and need
+                    for g, need in zip((gq, gk), ctx.needs_input_grad)]
+            grads = [rows(g) for g, w in zip((gq, gk), want) if w]
+            done = iter(())
+            if grads:
+                done = iter(tilemix_rope(
+                    grads[0], grads[1] if len(grads) > 1 else None,
+                    *ctx.saved_tensors, layout=layout, attn_factor=attn_factor,
+                    inverse=not inverse))
+            return (*(next(done) if w else None for w in want),
+                    None, None, None, None, None)
+
+    return Rope
+
+
 def tilemix_rope(q, k, positions, freqs, *, layout="half",
                  attn_factor: float = 1.0, inverse: bool = False, q_out=None,
                  k_out=None, stream=None):
     """Rotary positions of q [T, hq, d] and k [T, hkv, d] (k may be None) in
     one launch; fp16 or bf16, token and head strides free.  positions int32
     [T], freqs float64 [rot_dim / 2] on the device (channels past rot_dim are
-    copied).  `inverse` rotates back, which is also the gradient.  Outputs
-    default to new contiguous tensors; q_out=q rotates in place.
+    copied).  `inverse` rotates back, which is also the gradient; autograd
+    records it where q or k requires one (not with q_out or k_out given).
+    Outputs default to new contiguous tensors; q_out=q rotates in place.
     Returns (q_out, k_out)."""
     torch = _torch()
     index = q.get_device()
@@ -776,6 +815,13 @@ def tilemix_rope(q, k, positions, freqs, *, layout="half",
             return tilemix_rope(q, k, positions, freqs, layout=layout,
                                 attn_factor=attn_factor, inverse=inverse,
                                 q_out=q_out, k_out=k_out)
+    if torch.is_grad_enabled() and (q.requires_grad or
+                                    k is not None and k.requires_grad):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out take no part in autograd: leave "
+                             "them out, or call under torch.no_grad()")
+        return _rope_function().apply(q, k, positions, freqs, layout,
+                                      attn_factor, inverse)
     _check_device(index, "k positions freqs q_out k_out", k, positions, freqs,
                   q_out, k_out)
     dtype = q.dtype
@@ -826,7 +872,7 @@ def tilemix_paged_append(k, v, page_table, cu_seqlens, kv_lens, k_pages,
     type, or int8 with k_scale, v_scale fp32 [num_pages, hkv, page_size].
     With freqs, k (and q, if given) is rotated on the way, by each token's
     position in the cache or by `positions`.  Returns the rotated q (rows
-    past cu_seqlens[-1] are not written) or None."""
+    past cu_seqlens[-1] are not written) or None.  Records no gradient."""
     torch = _torch()
     index = k.get_device()
     ctx = _on(torch, index, stream)
@@ -909,7 +955,8 @@ def tilemix_attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens,
     new tokens and keys.  `workspace` (a CUDA tensor, 16-byte aligned, of
     tilemix_attn_paged_workspace_bytes) is allocated here when not given; two
     calls that may run at the same time need two.  Rows of q past
-    cu_seqlens[-1] are neither read nor written.  Returns out [T, hq, d]."""
+    cu_seqlens[-1] are neither read nor written.  Forward only: no gradient is
+    recorded.  Returns out [T, hq, d]."""
     torch = _torch()
     index = q.get_device()
     ctx = _on(torch, index, stream)

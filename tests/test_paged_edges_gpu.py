@@ -295,3 +295,81 @@ def test_attn_paged_bounds_beyond_32_bits_are_refused():
             tm.tilemix_attn_paged(q, k, v, table, cu, lens, a, b)
     with pytest.raises(tm.TilemixError):
         tm.tilemix_attn_paged(q, k, v, table, cu, lens, 1 << 30 | 1, 30)
+
+
+# ---------------------------------------------------------------------------
+# the rotation's gradient
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_rope_gradient_is_recorded(layout, dtype):
+    g = _gen(15)
+    qkv = torch.randn((9, 8, 64), generator=g).to(dtype).cuda().requires_grad_()
+    pos = torch.tensor([0, 1, 5, 77, 300, 4096, 9, 9, 100000], dtype=torch.int32)
+    f = torch.tensor([10000.0 ** (-i / 16.0) for i in range(16)],
+                     dtype=torch.float64)
+    go = torch.randn((9, 6, 64), generator=g).to(dtype)
+    kw = dict(layout=layout, attn_factor=1.25)
+    q, k = tm.tilemix_rope(qkv[:, :4], qkv[:, 4:6], pos.cuda(), f.cuda(), **kw)
+    plain, plain_k = tm.tilemix_rope(qkv.detach()[:, :4], qkv.detach()[:, 4:6],
+                                     pos.cuda(), f.cuda(), **kw)
+    assert torch.equal(q, plain) and torch.equal(k, plain_k)
+    assert q.requires_grad and k.requires_grad and not plain.requires_grad
+    (gx,) = torch.autograd.grad([q, k], [qkv], [go[:, :4].cuda(), go[:, 4:].cuda()],
+                                retain_graph=True)
+    want = oracle.rope(go, pos, f, layout, 1.25, True)
+    half = torch.finfo(dtype).eps / 2
+    # the rounded value, and fp32 cosines and sines of angles that are off by
+    # 2 pi 2^-26 and 3 2^-53 of up to 1e5 radians
+    tol = half * want.abs() + oracle.rope_bound(go, f, layout, 1.25, 1.2e-7) + 2.0 ** -25
+    assert ((gx[:, :6].cpu().double() - want).abs() <= tol).all()
+    assert (gx[:, 6:] == 0).all()
+    # one output only, expanded and misplaced gradients
+    (gq,) = torch.autograd.grad(q, [qkv], go[:, :4].cuda(), retain_graph=True)
+    assert torch.equal(gq[:, :4], gx[:, :4]) and (gq[:, 4:] == 0).all()
+    (gk,) = torch.autograd.grad(k, [qkv], go[:, 4:].cuda(), retain_graph=True)
+    assert torch.equal(gk[:, 4:6], gx[:, 4:6]) and (gk[:, :4] == 0).all()
+    ones = torch.ones_like(q)
+    (a,) = torch.autograd.grad(q, [qkv], ones, retain_graph=True)
+    (b,) = torch.autograd.grad(q.sum(), [qkv], retain_graph=True)
+    assert torch.equal(a, b)
+    odd = torch.randn((9 * 4 * 64 + 1,), generator=g).to(dtype).cuda()[1:].view(9, 4, 64)
+    (a,) = torch.autograd.grad(q, [qkv], odd, retain_graph=True)
+    (b,) = torch.autograd.grad(q, [qkv], odd.clone(), retain_graph=True)
+    assert torch.equal(a, b)
+    # the gradient's own gradient is the rotation
+    w = go[:, :4].cuda().requires_grad_()
+    (d,) = torch.autograd.grad(q, [qkv], w, create_graph=True)
+    (ww,) = torch.autograd.grad(d[:, :4], [w], qkv.detach()[:, :4])
+    assert torch.equal(ww, plain)
+
+
+def test_rope_gradient_without_k_streams_and_refusals():
+    x = torch.randn((5, 2, 64), generator=_gen(16)).half().cuda().requires_grad_()
+    pos = torch.arange(5, dtype=torch.int32).cuda()
+    f = torch.tensor([10000.0 ** (-i / 32.0) for i in range(32)],
+                     dtype=torch.float64).cuda()
+    y, none = tm.tilemix_rope(x, None, pos, f)
+    assert none is None
+    y.backward(torch.ones_like(y))
+    want, _ = tm.tilemix_rope(torch.ones_like(y).detach(), None, pos, f, inverse=True)
+    assert torch.equal(x.grad, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    z, _ = tm.tilemix_rope(x, None, pos, f, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    (gz,) = torch.autograd.grad(z, [x], torch.ones_like(z))
+    torch.cuda.synchronize()
+    assert torch.equal(z, y) and torch.equal(gz, want)
+    # k alone needs one
+    q = x.detach()
+    yq, yk = tm.tilemix_rope(q, x, pos, f)
+    (gk,) = torch.autograd.grad(yk, [x], torch.ones_like(yk))
+    assert torch.equal(gk, want) and torch.equal(yq, y)
+    with pytest.raises(ValueError, match="autograd"):
+        tm.tilemix_rope(x, None, pos, f, q_out=torch.empty_like(q))
+    with torch.no_grad():
+        out = torch.empty_like(q)
+        tm.tilemix_rope(x, None, pos, f, q_out=out)
+    assert torch.equal(out, y) and not out.requires_grad
