@@ -49,3 +49,39 @@ def test_exponential_on_the_fma_pipe():
     assert (_ex2_poly(np.array([-127.0, -np.inf, -1e30], F)) == 0).all()
     assert (_ex2_poly(np.arange(-126, 25).astype(F)) ==
             np.exp2(np.arange(-126, 25)).astype(F)).all()
+
+
+def _halves(dtype):
+    """Every positive finite value of fp16 or bf16, as float32."""
+    bits = np.arange(1, 1 << 15, dtype=np.uint32)
+    if dtype == "fp16":
+        x = bits.astype(np.uint16).view(np.float16).astype(F)
+    else:
+        x = (bits << 16).view(F)
+    return x[np.isfinite(x)]
+
+
+def test_int8_scale_against_the_quantisers():
+    # the append's scale a * fl(1 / 127) and the block quantiser's fl(a / 127):
+    # at most one step apart for every row maximum there is, and the row
+    # maximum's code is 127 under both
+    inv = F(1) / F(127)
+    for dtype in ("fp16", "bf16"):
+        a = _halves(dtype)
+        mul, div = a * inv, a / F(127)
+        assert (np.abs(mul - div) <= np.spacing(div)).all()
+        assert (mul > 0).all()
+        for s in (mul, div):
+            assert (np.rint(a / s) == 127).all()
+    # so a code moves by one at most, and only where x / scale lies within
+    # 127 * 2^-22 of a half
+    rng = np.random.default_rng(0)
+    xs = _halves("fp16")
+    for a in rng.choice(xs[xs > 2.0 ** -14], 200):
+        x = xs[xs <= a]
+        q = x / (a * inv)
+        c, d = np.rint(q), np.rint(x / (a / F(127)))
+        moved = c != d
+        assert (np.abs(c - d) <= 1).all()
+        assert (np.abs(np.abs(q[moved] - np.floor(q[moved])) - 0.5) <=
+                127 * 2.0 ** -22).all()

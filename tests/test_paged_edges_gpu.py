@@ -373,3 +373,91 @@ def test_rope_gradient_without_k_streams_and_refusals():
         out = torch.empty_like(q)
         tm.tilemix_rope(x, None, pos, f, q_out=out)
     assert torch.equal(out, y) and not out.requires_grad
+
+
+# ---------------------------------------------------------------------------
+# together with the prefill, and mixed batches
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+def test_prefill_attention_then_paged_decode(d, page, kv):
+    """A prompt goes through the prefill attention (all FP16) while its K and V
+    enter the pages; the paged attention of the same tokens agrees, and decoded
+    tokens continue over the pages."""
+    int8 = kv == "int8"
+    hq, hkv, n = 4, 2, [200, 131]
+    x = [torch.randn((m + 2, hq + 2 * hkv, d), generator=_gen(17 + m)).half()
+         for m in n]
+    pages = sum(-(-(m + 2) // page) for m in n)
+    kp = torch.zeros((pages, page, hkv, d), device="cuda",
+                     dtype=torch.int8 if int8 else torch.float16)
+    vp = torch.zeros_like(kp)
+    sc = dict(k_scale=torch.zeros((pages, hkv, page), device="cuda"),
+              v_scale=torch.zeros((pages, hkv, page), device="cuda")) if int8 else {}
+    first = -(-(n[0] + 2) // page)
+    order = list(range(pages))[::-1]
+    table = torch.tensor([order[:first], order[first:] + [-1] * (2 * first - pages)],
+                         dtype=torch.int32).cuda()
+    freqs, _ = tm.tilemix_rope_frequencies(d, 10000.0, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()
+    rot, outs = [[], []], [[], []]
+    for step, (a, b) in enumerate([(0, n), (n, [m + 1 for m in n]),
+                                   ([m + 1 for m in n], [m + 2 for m in n])]):
+        a = [0, 0] if a == 0 else a
+        y = torch.cat([x[s][a[s]:b[s]] for s in range(2)]).cuda()
+        new = [b[s] - a[s] for s in range(2)]
+        cu, ln = i32([0, new[0], sum(new)]), i32(b)
+        q = tm.tilemix_paged_append(
+            y[:, hq:hq + hkv], y[:, hq + hkv:], table, cu, ln, kp, vp,
+            q=y[:, :hq], freqs=freqs, **sc)
+        o = tm.tilemix_attn_paged(q, kp, vp, table, cu, ln, max(new), max(b), **sc)
+        if step == 0:
+            pos = torch.cat([torch.arange(m) for m in n]).int().cuda()
+            _, kr = tm.tilemix_rope(y[:, :hq], y[:, hq:hq + hkv], pos, freqs)
+            pre = tm.tilemix_attn_prefill(
+                q, kr, y[:, hq + hkv:].contiguous(), cu, max(n), fp16_only=True)
+            if not int8:
+                assert (pre.float() - o.float()).abs().max() <= 3e-3
+        for s, r in ((0, slice(0, new[0])), (1, slice(new[0], sum(new)))):
+            rot[s].append(q[r].cpu())
+            outs[s].append((o if int8 or step else pre)[r].cpu())
+    host = {name: t.cpu() for name, t in sc.items()}
+    for s in range(2):
+        m = n[s] + 2
+        want, _, tol = oracle.attn(torch.cat(rot[s]), kp.cpu(), vp.cpu(),
+                                   [table[s].tolist()], [0, m], [m], **host)
+        err = (torch.cat(outs[s]).double() - want).abs()
+        # (the prefill's rows to its own tolerance)
+        assert (err[n[s]:] <= tol[n[s]:]).all()
+        assert (err[:n[s]] <= (tol[:n[s]] if int8 else 3e-3)).all()
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+def test_attn_paged_one_chunk_among_single_tokens(kv):
+    new = [1] * 20 + [300] + [1] * 27
+    lens = [1 + 37 * b % 900 for b in range(48)]
+    lens[20] = 1400
+    c = Cache(lens, new, 2, 64, 32, torch.float16, kv == "int8", seed=18)
+    q = torch.randn((c.cu[-1] + 2, 4, 64), generator=_gen(19)).half()
+    _check_attn(c, q, True, pad=2)
+
+
+def test_attn_paged_repeats_exactly_on_other_memory():
+    # the same call again, on other memory: bit for bit the same
+    for new, n, hq, hkv, kv in ((1, 8191, 8, 8, True), (1, 4096, 8, 2, False),
+                                (5, 3000, 28, 4, False), (700, 2000, 6, 2, True),
+                                (700, 2000, 6, 2, False)):
+        c = Cache([n, n // 3], [new, min(new, n // 3)], hkv, 128, 64,
+                  torch.float16, kv, seed=n)
+        q = torch.randn((c.cu[-1], hq, 128), generator=_gen(n + 1)).half().cuda()
+        first = None
+        for _ in range(3):
+            k, v, table, cu, lens, sc = c.device()
+            keep = torch.full((1 << 22,), 3.0, device="cuda")
+            lse = torch.empty((hq, c.cu[-1]), device="cuda")
+            out = tm.tilemix_attn_paged(q, k, v, table, cu, lens, new, n, lse=lse,
+                                        **sc)
+            first = first or (out, lse)
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+            del keep
