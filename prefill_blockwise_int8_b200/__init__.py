@@ -699,7 +699,9 @@ def _cache(torch, k_pages, v_pages, k_scale, v_scale, page_table, cu_seqlens,
     if not int8 and kind is not dtype:
         raise ValueError(f"pages must be {dtype} or int8, got {kind}")
     strides = k_pages.stride()
-    if v_pages.stride() != strides:
+    if v_pages.stride() != strides and any(
+            a != b and m > 1
+            for a, b, m in zip(strides, v_pages.stride(), shape)):
         raise ValueError("k_pages and v_pages must share their strides")
     sp, st, sh, sd = strides
     if sd != 1 and d > 1:

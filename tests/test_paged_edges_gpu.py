@@ -461,3 +461,19 @@ def test_attn_paged_repeats_exactly_on_other_memory():
             first = first or (out, lse)
             assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
             del keep
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_strides_of_axes_of_one_do_not_matter(new):
+    # one KV head: token-major K and head-major V are the same layout
+    c = Cache([90], [new], 1, 64, 16, torch.float16, False, seed=20)
+    k, v, table, cu, lens, _ = c.device()
+    v = v.transpose(1, 2).contiguous().transpose(1, 2)
+    n, page, _, d = v.shape
+    v = v.as_strided((n, page, 1, d), (page * d, d, page * d, 1))
+    assert k.stride() != v.stride()
+    q = torch.randn((new, 4, 64), generator=_gen(21)).half()
+    _check_attn(c, q, True, device=(k, v, table, cu, lens, {}))
+    with pytest.raises(ValueError, match="strides"):
+        wide = torch.zeros((n, page, 1, 2 * d), dtype=v.dtype, device="cuda")
+        tm.tilemix_attn_paged(q.cuda(), k, wide[..., :d], table, cu, lens, new, 90)
