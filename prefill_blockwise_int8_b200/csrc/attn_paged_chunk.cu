@@ -34,8 +34,8 @@
 // (N = 64 products of shared memory run at 3/4 of the full rate; with 128-key
 // steps they take 1024, but P V and Q K^T then stand in the softmax's way and
 // a step is slower).  2048 tokens over 32768 keys, 32/8 heads, d 128, bf16:
-// 1.08 ms, 987 TFLOP/s; eight ragged chunks over INT8 keys, 24/8 heads: 0.575
-// ms, 485 TFLOP/s.
+// 1.08-1.12 ms back to back (by the clock), 950-990 TFLOP/s; eight ragged
+// chunks over INT8 keys, 24/8 heads: 0.578 ms, 482 TFLOP/s.
 #include <cuda.h>
 
 #include "attn_common.cuh"
@@ -71,9 +71,9 @@ struct Cfg {
   static constexpr float kLag = INT8 ? 11.0f : BF16 ? 24.0f : 15.0f;
   static constexpr float kScaleLag = 16.0f;
   // Of eight pairs of exponentials, how many run on the FMA pipe instead of
-  // the exponential unit: 2048 tokens over 32768 keys 956 us with none, 936
-  // with 2, 965 with 3; INT8, whose scales fill the FMA pipe, 530 with none,
-  // 545 with 2.
+  // the exponential unit: 2048 tokens over 32768 keys back to back 1114 us
+  // with none, 1098 with 1, 1096 with 2; INT8, whose scales fill the FMA pipe,
+  // 530 with none, 545 with 2 (single cold passes).
   static constexpr int kPolyOf8 = INT8 ? 0 : 2;
   static constexpr int kQTile = kM * D * 2;
   static constexpr int kTile = kN * D * 2;

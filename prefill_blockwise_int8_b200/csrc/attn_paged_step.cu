@@ -13,8 +13,8 @@
 // INT8 pages: K codes convert exactly to the query's 16-bit type and their
 // scale multiplies the fp32 score.  V codes convert exactly to fp16; their
 // scale joins P, which is then P sv 2^-E with 2^E the (lazily raised) power
-// of two above the scales seen, so that small scales do not fall into fp16
-// subnormals and large ones do not overflow.
+// of two above the sizes of the scales seen, so that small scales do not fall
+// into fp16 subnormals and large ones do not overflow.
 //
 // Work split.  All keys of all (sequence, KV head, 16-row tile) items, in
 // units of four groups, form one line; block c takes the c-th equal part of it.

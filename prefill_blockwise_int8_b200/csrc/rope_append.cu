@@ -15,8 +15,8 @@
 // heads) in shared memory, then every thread walks units of two 16-byte
 // vectors, which hold eight whole pairs in either layout, over the heads of
 // its token.  Rotating 32768 tokens of 24 + 8 heads, d 128: 92-97 us, 5.5-5.8
-// TB/s; the same with appending 16 prompts of 28 + 2 x 4 heads 240 us, 5.9
-// TB/s; 32768 tokens of 2 x 32 heads to INT8 pages 161 us, 5.0 TB/s.
+// TB/s; the same with appending 16 prompts of 28 + 2 x 4 heads 244 us, 5.9
+// TB/s; 32768 tokens of 2 x 32 heads to INT8 pages 165 us, 4.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
