@@ -477,3 +477,111 @@ def test_strides_of_axes_of_one_do_not_matter(new):
     with pytest.raises(ValueError, match="strides"):
         wide = torch.zeros((n, page, 1, 2 * d), dtype=v.dtype, device="cuda")
         tm.tilemix_attn_paged(q.cuda(), k, wide[..., :d], table, cu, lens, new, 90)
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_a_captured_serving_step_replays_over_a_growing_cache(new, kv):
+    """Append and attention in one captured graph: lengths move on the device,
+    every replay's tokens equal causal attention over all that was appended."""
+    int8 = kv == "int8"
+    hq, hkv, d, page, steps = 16, 2, 64, 16, 4
+    start = [30, 7]
+    pages = 30
+    kp = torch.zeros((pages, page, hkv, d), device="cuda",
+                     dtype=torch.int8 if int8 else torch.bfloat16)
+    vp = torch.zeros_like(kp)
+    sc = dict(k_scale=torch.zeros((pages, hkv, page), device="cuda"),
+              v_scale=torch.zeros((pages, hkv, page), device="cuda")) if int8 else {}
+    table = torch.randperm(pages, generator=_gen(31)).int().view(2, 15).cuda()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()
+    freqs, _ = tm.tilemix_rope_frequencies(d, 10000.0, device="cuda")
+    heads = hq + 2 * hkv
+    old = torch.randn((sum(start), heads, d), generator=_gen(32)).bfloat16().cuda()
+    lens = i32(start)
+    qs = [[], []]
+    q0 = tm.tilemix_paged_append(old[:, hq:hq + hkv], old[:, hq + hkv:], table,
+                                 i32([0, start[0], sum(start)]), lens, kp, vp,
+                                 q=old[:, :hq], freqs=freqs, **sc)
+    qs[0].append(q0[:start[0]].cpu())
+    qs[1].append(q0[start[0]:].cpu())
+    cu = i32([0, new, 2 * new])
+    x = torch.zeros((2 * new, heads, d), dtype=torch.bfloat16, device="cuda")
+    q = torch.empty((2 * new, hq, d), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(tm.tilemix_attn_paged_workspace_bytes(new, hq, hkv, d),
+                     dtype=torch.uint8, device="cuda")
+    most = max(start) + steps * new
+
+    def step():
+        lens.add_(new)
+        tm.tilemix_paged_append(x[:, hq:hq + hkv], x[:, hq + hkv:], table, cu, lens,
+                                kp, vp, q=x[:, :hq], q_out=q, freqs=freqs, **sc)
+        tm.tilemix_attn_paged(q, kp, vp, table, cu, lens, new, most, out=out,
+                              workspace=ws, **sc)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    outs = [[], []]
+    for s in range(steps):
+        x.copy_(torch.randn(x.shape, generator=_gen(40 + s)))
+        graph.replay()
+        for b in range(2):
+            qs[b].append(q[b * new:(b + 1) * new].cpu())
+            outs[b].append(out[b * new:(b + 1) * new].cpu())
+    assert lens.tolist() == [n + steps * new for n in start]
+    for b in range(2):
+        n = start[b] + steps * new
+        want, _, tol = oracle.attn(
+            torch.cat(qs[b]), kp.cpu(), vp.cpu(), [table[b].tolist()], [0, n], [n],
+            **{name: t.cpu() for name, t in sc.items()})
+        err = (torch.cat(outs[b]).double() - want[start[b]:]).abs()
+        assert (err <= tol[start[b]:]).all()
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+@pytest.mark.parametrize("new", [1, 50])
+def test_sequences_that_share_pages(new, kv):
+    # one prompt's pages in every row of the table, lengths of their own
+    c = Cache([500], [new], 2, 64, 16, torch.float16, kv == "int8", seed=51)
+    c.table = c.table.repeat(3, 1)
+    c.lens, c.new = [500, 77 + new, 320], [new] * 3
+    c.cu = [0, new, 2 * new, 3 * new]
+    q = torch.randn((3 * new, 8, 64), generator=_gen(52)).half()
+    _check_attn(c, q, True)
+
+
+@pytest.mark.parametrize("kv", ["same", "int8"])
+def test_two_caches_grow_on_two_streams_at_once(kv):
+    caches = [Cache([900, 40], [600, 40], 2, 128, 32, torch.float16, kv == "int8",
+                    seed=60 + i, poison=False) for i in range(2)]
+    x = torch.randn((640, 12, 128), generator=_gen(61)).half().cuda()
+    f = torch.tensor([10000.0 ** (-i / 64.0) for i in range(64)],
+                     dtype=torch.float64).cuda()
+
+    def step(dev, stream):
+        k, v, table, cu, lens, sc = dev
+        q = tm.tilemix_paged_append(x[:, 8:10], x[:, 10:], table, cu, lens, k, v,
+                                    q=x[:, :8], freqs=f, stream=stream, **sc)
+        return q, tm.tilemix_attn_paged(q, k, v, table, cu, lens, 600, 900,
+                                        stream=stream, **sc)
+
+    plain = [c.device() for c in caches]
+    want = [step(dev, None) for dev in plain]
+    both = [c.device() for c in caches]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(3):  # appending the same tokens again changes nothing
+        for i in range(2):
+            got[i] = step(both[i], streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b in zip(want[i], got[i]):
+            assert torch.equal(a, b)
+        for a, b in zip(plain[i][:2], both[i][:2]):
+            assert torch.equal(a, b)
+        for name, t in plain[i][5].items():
+            assert torch.equal(t, both[i][5][name])
