@@ -110,10 +110,18 @@ bool too_many_rows(int max_q_len, int group) {
 }
 
 // Which attention kernel: the step kernel reads the cache once per 16 packed
-// rows, the chunk kernel once per 256 but with more to begin and end.  16
-// sequences of 6000 keys, d 128, step against chunk: 16 rows 50 / 49 us, 24
-// rows 75 / 49; 4000 keys of one sequence 8 rows 19 / 21.  INT8, whose chunk
-// kernel converts tiles first: 16 rows 49 / 88, 32 rows 71 / 89.
+// rows, the chunk kernel once per 256 but with more to begin and end.  Step
+// against chunk, us in a graph, 8 KV heads, at 16 / 24 rows (INT8, whose chunk
+// kernel converts tiles first: at 16 / 32):
+//                          d 64                    d 128
+//   16 x 6000 keys   49 : 62 / 67 : 62       77 : 75 / 125 : 76
+//   1 x 32000        23 : 30 / 27 : 30       37 : 38 / 54 : 38
+//   64 x 1000        41 : 56 / 61 : 56       60 : 66 / 99 : 67
+//   4 x 500          13 : 13 / 13 : 13       13 : 14 / 16 : 14
+//   INT8 16 x 6000   39 : 109 / 61 : 110     58 : 128 / 93 : 129
+//   INT8 1 x 32000   26 : 47 / 31 : 47       32 : 50 / 42 : 51
+//   INT8 64 x 1000   35 : 106 / 55 : 106     54 : 131 / 84 : 132
+//   INT8 4 x 500     13 : 17 / 14 : 17       16 : 18 / 17 : 19
 bool use_step(int max_q_len, int group, bool int8) {
   return static_cast<long long>(max_q_len) * group <= (int8 ? 32 : 16);
 }
