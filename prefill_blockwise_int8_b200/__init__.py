@@ -806,7 +806,10 @@ def tilemix_rope(q, k, positions, freqs, *, layout="half",
     one launch; fp16 or bf16, token and head strides free.  positions int32
     [T], freqs float64 [rot_dim / 2] on the device (channels past rot_dim are
     copied).  `inverse` rotates back, which is also the gradient; autograd
-    records it where q or k requires one (not with q_out or k_out given).
+    records it where q or k requires one (not with q_out or k_out given;
+    positions and freqs are constants).  As with any torch operation, a
+    backward pass goes into a CUDA graph only while no earlier result of the
+    same leaves is alive.
     Outputs default to new contiguous tensors; q_out=q rotates in place.
     Returns (q_out, k_out)."""
     torch = _torch()
